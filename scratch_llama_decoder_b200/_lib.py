@@ -59,8 +59,21 @@ class llm_lr_schedule(C.Structure):
                 ("decay_start", C.c_int64), ("total_steps", C.c_int64), ("shape", C.c_int32)]
 
 
+# element formats and error bits of the paged cache (include/llm_kernels.h)
+LLM_KV_F32, LLM_KV_BF16, LLM_KV_E4M3, LLM_KV_INT8 = 0, 1, 2, 3
+LLM_PACKED_BAD_CU, LLM_KV_BAD_PAGE, LLM_PACKED_TIMEOUT = 1, 2, 4
+
+
+class llm_kv(C.Structure):
+    _fields_ = [("d_pages", C.c_void_p), ("d_scales", C.c_void_p), ("d_table", C.c_void_p),
+                ("table_ld", C.c_int64), ("n_pages", C.c_int64), ("table_pages", C.c_int32),
+                ("format", C.c_int32), ("n_kv_head", C.c_int32), ("head_dim", C.c_int32),
+                ("page_size", C.c_int32), ("d_flag", C.c_void_p)]
+
+
 _vp, _i64, _u64, _f, _i = C.c_void_p, C.c_int64, C.c_uint64, C.c_float, C.c_int
 _cfgp = C.POINTER(llm_config)
+_kvp = C.POINTER(llm_kv)
 
 EXPORTS = {
     "llm_param_layout": (_i, [_cfgp, C.POINTER(llm_tensor_info), C.POINTER(_i), C.POINTER(_i64)]),
@@ -118,6 +131,16 @@ EXPORTS = {
     "llm_kernel_embed_bwd_scratch_bytes": (_i, [_i64, _i, C.POINTER(_i64)]),
     "llm_kernel_embed_bwd": (_i, [_vp, _vp, _vp, _i64, _i, _i, _vp, _i64, _vp]),
     "llm_kernel_embed_bwd_noalloc": (_i, [_vp, _vp, _vp, _i64, _i, _i, _vp]),
+    "llm_kernel_attention_packed_workspace": (_i, [_i64, _i, _i, _i, C.POINTER(_i64)]),
+    "llm_kernel_attention_packed_fwd": (_i, [_vp, _i64, _i, _vp, _i, _i64, _i, _i, _i, _vp, _vp,
+                                             _vp, _i64, _vp, _vp]),
+    "llm_kernel_attention_packed_bwd": (_i, [_vp, _i64, _i, _vp, _i, _i64, _i, _i, _i, _vp, _vp,
+                                             _vp, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "llm_kernel_kv_write": (_i, [_kvp, _vp, _i64, _i, _vp, _vp, _i, _i64, _i, _vp]),
+    "llm_kernel_kv_read": (_i, [_kvp, _vp, _vp, _i, _i64, _vp, _vp, _i, _vp]),
+    "llm_kernel_attention_paged_workspace": (_i, [_kvp, _i, _i, C.POINTER(_i64)]),
+    "llm_kernel_attention_paged": (_i, [_kvp, _vp, _i64, _i, _vp, _i, _i, _vp, _vp, _vp, _i64,
+                                        _vp]),
 }
 for _name, (_res, _args) in EXPORTS.items():
     _fn = getattr(lib, _name)

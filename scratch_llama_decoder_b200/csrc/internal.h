@@ -250,6 +250,10 @@ bool smem_optin(const void *func, int bytes);
 // Streaming multiprocessors of the current device (cached per device).
 int device_sms();
 
+// The process's one device: the first call fixes it; false when another
+// device is current (or none).  *dev, when given, receives it.
+bool claim_device(int *dev);
+
 // Launch counter (kernels enqueued by the current call).
 extern thread_local int g_launches;
 inline void count_launch(int n = 1) { g_launches += n; }

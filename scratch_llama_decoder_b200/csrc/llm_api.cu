@@ -351,7 +351,8 @@ int llm_workspace_bytes(const llm_config *cfg, int64_t *bytes) {
 // call that needs a device fixes it, later calls with another device current
 // are refused.
 static std::atomic<int> g_device{-1};
-static bool claim_device(int *dev) {
+extern "C++" {
+bool llm::claim_device(int *dev) {
   int d = -1;
   if (cudaGetDevice(&d) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -361,6 +362,7 @@ static bool claim_device(int *dev) {
   if (!g_device.compare_exchange_strong(first, d) && first != d) return false;
   if (dev) *dev = d;
   return true;
+}
 }
 // The context's device is the current one.
 static bool on_device(const llm_ctx *c) {

@@ -1,0 +1,67 @@
+// Packed sequences: rows of several sequences end to end in one array, rows
+// [cu[s], cu[s+1]) belonging to sequence s.  Shared by the packed attention
+// kernels (work plan in the caller's workspace) and the paged cache.
+#pragma once
+#include "common.cuh"
+
+namespace llm {
+
+constexpr int PK_BLOCK = 128;             // rows of a work tile
+constexpr int64_t PK_MAX_ROWS = 1 << 20;  // packed rows of one call
+constexpr int PK_MAX_SEQ = 65536;         // sequences of one call
+// bits OR-ed into the caller's flag word (FLAG_TIMEOUT is bit 4)
+enum : int { PK_BAD_OFFSETS = 1, PK_BAD_PAGE = 2 };
+
+// One 128-row tile of a sequence: first packed row and length of the
+// sequence, block index within it.  As a key tile the same entry stands for
+// block n - 1 - blk (n blocks), whose query blocks are as many.
+struct PkTile {
+  int row0, len, blk, pad;
+};
+// The workspace: tile count, then the tiles (most work first), then scratch
+// of the plan (clamped offsets, ranks), then D of the backward.
+struct PkPlan {
+  int *n_tiles;
+  PkTile *tiles;
+  int *off, *rank;
+  float *D;
+  int64_t cap, bytes;
+};
+inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward) {
+  PkPlan p;
+  uint8_t *b = (uint8_t *)ws;
+  const int64_t nonempty = n_seq < n_rows ? n_seq : n_rows;
+  p.cap = n_rows / PK_BLOCK + nonempty;
+  int64_t at = 0;
+  auto take = [&](int64_t n) {
+    uint8_t *q = b + at;
+    at = (at + n + 255) / 256 * 256;
+    return q;
+  };
+  p.n_tiles = (int *)take(4);
+  p.tiles = (PkTile *)take(p.cap * (int64_t)sizeof(PkTile));
+  p.off = (int *)take(4 * ((int64_t)n_seq + 1));
+  p.rank = (int *)take(4 * (int64_t)n_seq);
+  p.D = (float *)take(backward ? 4 * n_rows * H : 0);
+  p.bytes = at;
+  return p;
+}
+
+struct PkArgs {
+  const void *qkv;
+  int64_t ld;
+  DType dt;
+  const int32_t *cu;
+  int n_seq;
+  int64_t n_rows;
+  int H, Hkv, hd;
+  int *flag;  // device word, may be null
+  cudaStream_t s;
+};
+void packed_plan(const PkArgs &a, const PkPlan &p);
+// CUDA-core kernels: float32 arithmetic, either type, head sizes to 128.
+bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse);
+bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
+                     const void *dout, void *dqkv, int64_t dld);
+
+}  // namespace llm
