@@ -145,13 +145,16 @@ LLM_DEV void tmem_free_512(uint32_t tmem) {
 // S/dP and dS barriers count key blocks over all of a CTA's items (gb), so
 // the next item's tiles land and its first products run while this item's
 // last blocks and epilogue are still in flight.
+// PK: the items are the tiles of a packed plan (pk) and T the length of the
+// item's own sequence.
+template <bool PK>
 __global__ void __launch_bounds__(NTHREADS, 1)
     k_attn_dq_tc(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_do,
                  const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_st,
                  const float *__restrict__ lse,
                  float *__restrict__ Dv, __nv_bfloat16 *__restrict__ dqkv,
-                 const float *__restrict__ cos_t, const float *__restrict__ sin_t, int B, int T,
-                 int H, int Hkv, int hd, float scale, int bulk_l, int *gflag) {
+                 const float *__restrict__ cos_t, const float *__restrict__ sin_t, int B, int T_all,
+                 int H, int Hkv, int hd, float scale, int bulk_l, const PkView pk, int *gflag) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sQ = smem, *sdO = smem + 2 * TILE_BYTES, *sO = smem + 4 * TILE_BYTES,
@@ -174,16 +177,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  qred = qsync + 32;       // [4]: per lane quarter, its rows' D parts written
   static_assert(6 + 4 * STAGES + 18 <= 48, "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int nqb = (T + BQ - 1) / BQ, n_items = nqb * H * B;
+  const int nqb = (T_all + BQ - 1) / BQ, n_items = PK ? *pk.n_tiles * H : nqb * H * B;
   const int G = gridDim.x, cta = blockIdx.x;
   // item -> (query block, head, batch): longest rows (last query blocks) first,
   // in bands of 4 query blocks taken pair by pair (band_item)
-  auto decode = [&](int item, int &qb, int &h, int &b) {
+  auto decode = [&](int item) {
+    if constexpr (PK) return pk_item(pk, item, H, false);
     int z, pr;
     band_item(item, nqb, H * B, z, pr);
-    qb = nqb - 1 - z;
-    h = pr % H;
-    b = pr / H;
+    return Item{nqb - 1 - z, pr % H, pr / H, pr / H * T_all, T_all};
+  };
+  // first element of the item's lse and D rows
+  auto stat = [&](const Item &im, int h) {
+    return PK ? h * pk.n_rows + im.row0 : ((int64_t)im.b * H + h) * im.T;
   };
 
   if (threadIdx.x == 0) {
@@ -229,9 +235,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int r = 0, it = 0; ok; r++, it++) {
       const int item = sched_item(r, G, cta);
       if (item >= n_items) break;
-      int qb, h, b;
-      decode(item, qb, h, b);
-      const int q0 = qb * BQ, row_base = b * T, g = h / (H / Hkv), slot = it & 1;
+      const Item im = decode(item);
+      const int qb = im.blk, h = im.h, T = im.T;
+      const int q0 = qb * BQ, row_base = im.row0, g = h / (H / Hkv), slot = it & 1;
       // Q, dO into the slot of item it - 2 once it was released
       if (!warp_wait(qd_empty + 8 * slot, ((it >> 1) & 1) ^ 1, abort_sh, gflag)) break;
       if (lane == 0) {
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // by a bulk copy when its rows are 16-byte aligned (T % 4 == 0), else
       // by the lanes
       if (!warp_wait(o_empty, (it & 1) ^ 1, abort_sh, gflag)) break;
-      const float *lrow = lse + ((int64_t)b * H + h) * T + q0;
+      const float *lrow = lse + stat(im, h) + q0;
       const int nvalid = min(BQ, T - q0);
       if (lane == 0) {
         mbar_arrive_expect_tx(o_full, TILE_BYTES + (bulk_l ? nvalid * 4 : 0));
@@ -310,8 +316,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int gb = 0;
     int item = sched_item(0, G, cta);
     if (item < n_items) {  // products of the first block
-      int qb, h, b;
-      decode(item, qb, h, b);
+      const int qb = decode(item).blk;
       ok = warp_wait(qd_full, 0, abort_sh, gflag) && warp_wait(b_full, 0, abort_sh, gflag);
       if (ok) {
         fence_after();
@@ -320,12 +325,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     for (int r = 0, it = 0; item < n_items && ok; r++, it++) {
-      int qb, h, b;
-      decode(item, qb, h, b);
-      const int nj = qb + 1, slot = it & 1;
+      const int nj = decode(item).blk + 1, slot = it & 1;
       const int next = sched_item(r + 1, G, cta);
-      int qb_next = 0, hn, bn;
-      if (next < n_items) decode(next, qb_next, hn, bn);
+      const int qb_next = next < n_items ? decode(next).blk : 0;
       for (int j = 0; j < nj && ok; j++, gb++) {
         const int s = gb % STAGES;
         const uint32_t ph = (gb / STAGES) & 1;
@@ -381,8 +383,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int rr = 0, it = 0; ok; rr++, it++) {
       const int item = sched_item(rr, G, cta);
       if (item >= n_items) break;
-      int qb, h, b;
-      decode(item, qb, h, b);
+      const Item im = decode(item);
+      const int qb = im.blk, h = im.h, b = im.b, T = im.T;
       const int q0 = qb * BQ, nj = qb + 1, slot = it & 1;
       const int qi = q0 + r;
       const bool valid = qi < T;
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         st_slot = -1;
       }
-      if (cq == 0 && valid) Dv[((int64_t)b * H + h) * T + qi] = Di;
+      if (cq == 0 && valid) Dv[stat(im, h) + qi] = Di;
       const float2 nl = make_float2(nl2, nl2), nd = make_float2(-Di, -Di);
       for (int j = 0; j < nj && ok; j++, gb++) {
         if (!warp_wait(s_full, gb & 1, abort_sh, gflag)) {
@@ -458,7 +460,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 __ffma2_rn(make_float2(sv[i], sv[i + 1]), make_float2(sl2, sl2), nl), i / 2);
             if (k0 + i > qi) p.x = 0.f;
             if (k0 + i + 1 > qi) p.y = 0.f;
-            const float2 ds = __fmul2_rn(p, __fadd2_rn(make_float2(dv[i], dv[i + 1]), nd));
+            float2 ds = __fmul2_rn(p, __fadd2_rn(make_float2(dv[i], dv[i + 1]), nd));
+            if constexpr (PK) {  // dP of a key past the sequence may be no number
+              if (k0 + i > qi) ds.x = 0.f;
+              if (k0 + i + 1 > qi) ds.y = 0.f;
+            }
             w[i / 2] = pack_bf16(ds.x, ds.y);
           }
         } else {
@@ -484,6 +490,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tmem_stn<(CW / 2 < 16 ? CW / 2 : 16)>(tmem + lane_off + DQ_COL_DS + cq * (CW / 2) + c,
                                                w + c);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        if constexpr (PK) {  // this group's K rows past the sequence's end
+          if (k0 + CW > T) {
+            const int s = gb % STAGES;
+            if (!warp_wait(k_full + 8 * s, (gb / STAGES) & 1, abort_sh, gflag)) {
+              ok = false;
+              break;
+            }
+            zero_rows(sK + s * TILE_BYTES + cq * CW * 128, T - k0, r);
+          }
+        }
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full + 8 * x);
@@ -542,10 +558,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ok = false;
         break;
       }
-      if (lane == 0) {
-        const int r0 = quarter * 32 + cq * 8;
-        tma_store_4d(&tm_st, smem_u32(sQ + slot * TILE_BYTES + r0 * 128), 0, h, q0 + r0, b);
-        bulk_commit();
+      const int r0 = quarter * 32 + cq * 8;
+      if (!PK || q0 + r0 + 8 <= T) {
+        if (lane == 0) {
+          tma_store_4d(&tm_st, smem_u32(sQ + slot * TILE_BYTES + r0 * 128), 0, h,
+                       PK ? im.row0 + q0 + r0 : q0 + r0, b);
+          bulk_commit();
+        }
+      } else {  // a piece that the sequence's end cuts, row by row
+        store_cut(sQ + slot * TILE_BYTES, r0, T - q0,
+                  pk.out + (im.row0 + q0 + r0) * pk.out_ld + h * hd, pk.out_ld, hd, lane);
       }
       st_slot = slot;  // released (below) once the store has read the tile
     }
@@ -563,13 +585,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // the (query head, query block) steps of all of a CTA's items through one
 // ring (global step gs), so the next item's first products start while this
 // item's last accumulations and epilogue run.
+template <bool PK>
 __global__ void __launch_bounds__(NTHREADS, 1)
     k_attn_dkv_tc(const __grid_constant__ CUtensorMap tm_qkv,
                   const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_st,
                   const float *__restrict__ lse,
                   const float *__restrict__ Dv, __nv_bfloat16 *__restrict__ dqkv,
-                  const float *__restrict__ cos_t, const float *__restrict__ sin_t, int B, int T,
-                  int H, int Hkv, int hd, float scale, int bulk_l, int *gflag) {
+                  const float *__restrict__ cos_t, const float *__restrict__ sin_t, int B, int T_all,
+                  int H, int Hkv, int hd, float scale, int bulk_l, const PkView pk, int *gflag) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sK = smem, *sV = smem + 2 * TILE_BYTES, *sQ = smem + 4 * TILE_BYTES,
@@ -588,17 +611,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  qsync = drain + 16;   // [4]: per lane quarter, its rows of dK, dV staged
   static_assert(4 + 3 * STAGES + 10 <= 48, "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int nkb = (T + BK - 1) / BK, n_items = nkb * Hkv * B;
+  const int nkb_all = (T_all + BK - 1) / BK, n_items = PK ? *pk.n_tiles * Hkv : nkb_all * Hkv * B;
   const int G = gridDim.x, cta = blockIdx.x;
   const int grp = H / Hkv;
   // item -> (key block, kv head, batch), first key blocks first in bands of 4
   // taken pair by pair (band_item); steps = grp (nkb - kb)
-  auto decode = [&](int item, int &kb, int &g, int &b) {
-    int pr;
-    band_item(item, nkb, Hkv * B, kb, pr);
-    g = pr % Hkv;
-    b = pr / Hkv;
+  auto decode = [&](int item) {
+    if constexpr (PK) return pk_item(pk, item, Hkv, true);
+    int kb, pr;
+    band_item(item, nkb_all, Hkv * B, kb, pr);
+    return Item{kb, pr % Hkv, pr / Hkv, pr / Hkv * T_all, T_all};
   };
+  auto blocks = [&](const Item &im) { return (im.T + BK - 1) / BK; };
 
   if (threadIdx.x == 0) {
     *abort_sh = 0;
@@ -635,9 +659,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int r = 0, it = 0; ok; r++, it++) {
       const int item = sched_item(r, G, cta);
       if (item >= n_items) break;
-      int kb, g, b;
-      decode(item, kb, g, b);
-      const int k0 = kb * BK, row_base = b * T, nq = nkb - kb, slot = it & 1;
+      const Item im = decode(item);
+      const int kb = im.blk, g = im.h, T = im.T;
+      const int k0 = kb * BK, row_base = im.row0, nq = blocks(im) - kb, slot = it & 1;
       if (!warp_wait(kv_empty + 8 * slot, ((it >> 1) & 1) ^ 1, abort_sh, gflag)) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(kv_full + 8 * slot, 2 * TILE_BYTES);
@@ -659,7 +683,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // the step's L and D rows by bulk copies when 16-byte aligned (T % 4
         // == 0), else by the lanes; queries past T get L = +inf, so their P is
         // 0 (below 2^-125 where the polynomial exponential takes the pair), and D = 0
-        const int64_t base = ((int64_t)b * H + hq) * T + qb * BQ;
+        const int64_t base =
+            (PK ? hq * pk.n_rows + im.row0 : ((int64_t)im.b * H + hq) * T) + qb * BQ;
         const int nvalid = min(BQ, T - qb * BQ);
         if (lane == 0) {
           mbar_arrive_expect_tx(q_full + 8 * s, 2 * TILE_BYTES + (bulk_l ? 8 * nvalid : 0));
@@ -716,23 +741,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int gs = 0;
     int item = sched_item(0, G, cta);
     if (item < n_items) {  // products of the first step
-      int kb, g, b;
-      decode(item, kb, g, b);
+      const Item im = decode(item);
       ok = warp_wait(kv_full, 0, abort_sh, gflag) && warp_wait(q_full, 0, abort_sh, gflag);
       if (ok) {
         fence_after();
         issue_prod(0, 0);
-        if (grp * (nkb - kb) == 1) mma_commit_e(kv_empty);  // the item's last products on slot 0
+        if (grp * (blocks(im) - im.blk) == 1) mma_commit_e(kv_empty);  // the item's last products on slot 0
       }
     }
     for (int r = 0, it = 0; item < n_items && ok; r++, it++) {
-      int kb, g, b;
-      decode(item, kb, g, b);
-      const int nsteps = grp * (nkb - kb), slot = it & 1;
+      const Item im = decode(item);
+      const int nsteps = grp * (blocks(im) - im.blk), slot = it & 1;
       const int next = sched_item(r + 1, G, cta);
-      int kb_next = nkb - 1, gn, bn;
-      if (next < n_items) decode(next, kb_next, gn, bn);
-      const int nsteps_next = grp * (nkb - kb_next);
+      int nsteps_next = grp;
+      if (next < n_items) {
+        const Item in = decode(next);
+        nsteps_next = grp * (blocks(in) - in.blk);
+      }
       for (int st = 0; st < nsteps && ok; st++, gs++) {
         const int s = gs % STAGES;
         // products of step gs + 1 (this item's next, or the next item's first)
@@ -783,9 +808,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int rr = 0, it = 0; ok; rr++, it++) {
       const int item = sched_item(rr, G, cta);
       if (item >= n_items) break;
-      int kb, g, b;
-      decode(item, kb, g, b);
-      const int k0 = kb * BK, kj = k0 + r, nq = nkb - kb, slot = it & 1;
+      const Item im = decode(item);
+      const int kb = im.blk, g = im.h, b = im.b, T = im.T;
+      const int k0 = kb * BK, kj = k0 + r, nq = blocks(im) - kb, slot = it & 1;
       const int nsteps = grp * nq;
       // the accumulators of the previous item were read out before this
       // warp's first P^T / dS^T arrival below (program order), so the
@@ -847,6 +872,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             wd[i / 2] = pack_bf16(d01.x, d01.y);
             wd[i / 2 + 1] = pack_bf16(d23.x, d23.y);
           }
+          if constexpr (PK) {
+            // queries past the sequence's end, and what the causal mask puts
+            // to 0 beside a dP that may be no number
+            if (diag || qc0 + CW > T) {
+#pragma unroll
+              for (int i = 0; i < HC; i += 2) {
+                const int q = qc0 + hf * HC + i;
+                const uint32_t keep = (q < T && kj <= q ? 0xffffu : 0u) |
+                                      (q + 1 < T && kj <= q + 1 ? 0xffff0000u : 0u);
+                wp[i / 2] &= keep;
+                wd[i / 2] &= keep;
+              }
+            }
+          }
           if (hf == 0 && st > 0) {
             if (!warp_wait(pv_done, (gs - 1) & 1, abort_sh, gflag)) {
               ok = false;
@@ -859,6 +898,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!ok) break;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        if constexpr (PK) {  // this group's rows of Q and dO past the sequence's end
+          if (qc0 + CW > T) {
+            zero_rows(sQ + s * TILE_BYTES + cq * CW * 128, T - qc0, r);
+            zero_rows(sdO + s * TILE_BYTES + cq * CW * 128, T - qc0, r);
+          }
+        }
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
@@ -919,12 +964,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ok = false;
         break;
       }
-      if (lane == 0) {
-        const int r0 = quarter * 32 + cq * 8;
-        tma_store_4d(&tm_st, smem_u32(sK + slot * TILE_BYTES + r0 * 128), 0, H + g, k0 + r0, b);
-        tma_store_4d(&tm_st, smem_u32(sV + slot * TILE_BYTES + r0 * 128), 0, H + Hkv + g, k0 + r0,
-                     b);
-        bulk_commit();
+      const int r0 = quarter * 32 + cq * 8;
+      if (!PK || k0 + r0 + 8 <= T) {
+        if (lane == 0) {
+          const int row = PK ? im.row0 + k0 + r0 : k0 + r0;
+          tma_store_4d(&tm_st, smem_u32(sK + slot * TILE_BYTES + r0 * 128), 0, H + g, row, b);
+          tma_store_4d(&tm_st, smem_u32(sV + slot * TILE_BYTES + r0 * 128), 0, H + Hkv + g, row,
+                       b);
+          bulk_commit();
+        }
+      } else {  // a piece that the sequence's end cuts, row by row
+        __nv_bfloat16 *dst = pk.out + (im.row0 + k0 + r0) * pk.out_ld + (H + g) * hd;
+        store_cut(sK + slot * TILE_BYTES, r0, T - k0, dst, pk.out_ld, hd, lane);
+        store_cut(sV + slot * TILE_BYTES, r0, T - k0, dst + Hkv * hd, pk.out_ld, hd, lane);
       }
       st_slot = slot;  // released after the next item's first step
     }
@@ -950,8 +1002,8 @@ bool attn_bwd_tc(const void *qkv, const void *o, const void *dout, const float *
   if ((hd != 64 && hd != 32) || !flag || ((uintptr_t)o & 15) || ((uintptr_t)dqkv & 15) ||
       ((uintptr_t)cos_t & 15) || ((uintptr_t)sin_t & 15) || (!cos_t != !sin_t))
     return false;
-  if (!smem_optin((const void *)k_attn_dq_tc, DQ_SMEM) ||
-      !smem_optin((const void *)k_attn_dkv_tc, KV_SMEM))
+  if (!smem_optin((const void *)k_attn_dq_tc<false>, DQ_SMEM) ||
+      !smem_optin((const void *)k_attn_dkv_tc<false>, KV_SMEM))
     return false;
   const int64_t qkvw = (int64_t)(H + 2 * Hkv) * hd, dw = (int64_t)H * hd;
   CUtensorMap mq, md, mo, mst;
@@ -964,12 +1016,41 @@ bool attn_bwd_tc(const void *qkv, const void *o, const void *dout, const float *
   const float scale = 1.0f / sqrtf((float)hd);
   // L and D rows of a (batch, head) start 16-byte aligned when T % 4 == 0
   const int bulk_l = (T % 4 == 0) && !((uintptr_t)lse & 15) && !((uintptr_t)Dbuf & 15);
-  k_attn_dq_tc<<<min(nb * H * B, sms), NTHREADS, DQ_SMEM, s>>>(
+  k_attn_dq_tc<false><<<min(nb * H * B, sms), NTHREADS, DQ_SMEM, s>>>(
       mq, md, mo, mst, lse, Dbuf, (__nv_bfloat16 *)dqkv, cos_t, sin_t, B, T, H, Hkv, hd, scale,
-      bulk_l, flag);
-  k_attn_dkv_tc<<<min(nb * Hkv * B, sms), NTHREADS, KV_SMEM, s>>>(
+      bulk_l, PkView{}, flag);
+  k_attn_dkv_tc<false><<<min(nb * Hkv * B, sms), NTHREADS, KV_SMEM, s>>>(
       mq, md, mst, lse, Dbuf, (__nv_bfloat16 *)dqkv, cos_t, sin_t, B, T, H, Hkv, hd, scale,
-      bulk_l, flag);
+      bulk_l, PkView{}, flag);
+  count_launch(2);
+  return true;
+}
+
+// The same kernels over the tiles of a packed plan.
+bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
+                   const void *dout, void *dqkv, int64_t dld, int *flag) {
+  using namespace attn_tc_bwd;
+  if (a.dt != DT_BF16 || (a.hd != 64 && a.hd != 32)) return false;
+  if (!smem_optin((const void *)k_attn_dq_tc<true>, DQ_SMEM) ||
+      !smem_optin((const void *)k_attn_dkv_tc<true>, KV_SMEM))
+    return false;
+  const int64_t dw = (int64_t)a.H * a.hd;
+  CUtensorMap mq, md, mo, mst;
+  if (!head_map_load(&mq, a.qkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, a.ld, 128) ||
+      !head_map_load(&md, dout, a.hd, a.H, a.n_rows, dw, 128) ||
+      !head_map_load(&mo, o, a.hd, a.H, a.n_rows, dw, 128) ||
+      !head_map_store(&mst, dqkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, 1, dld, 8))
+    return false;
+  const int64_t sms = device_sms();
+  const float scale = 1.0f / sqrtf((float)a.hd);
+  const PkView pk{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)dqkv, dld};
+  // L and D rows start anywhere: read by the lanes
+  k_attn_dq_tc<true><<<(int)min(p.cap * a.H, sms), NTHREADS, DQ_SMEM, a.s>>>(
+      mq, md, mo, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H, a.Hkv, a.hd,
+      scale, 0, pk, flag);
+  k_attn_dkv_tc<true><<<(int)min(p.cap * a.Hkv, sms), NTHREADS, KV_SMEM, a.s>>>(
+      mq, md, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H, a.Hkv, a.hd,
+      scale, 0, pk, flag);
   count_launch(2);
   return true;
 }

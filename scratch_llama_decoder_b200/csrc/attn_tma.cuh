@@ -16,10 +16,56 @@
 
 #include <cstdint>
 
-#include "common.cuh"
+#include "packed.cuh"
+#include "tcgen05.cuh"
 
 namespace llm {
 namespace attn_maps {
+
+// What a kernel over packed sequences gets besides the tensor maps: the work
+// plan, the row count (stride of the heads in lse and D) and the output rows
+// for tiles that a sequence's end cuts.
+struct PkView {
+  const int *n_tiles;
+  const PkTile *tiles;
+  int64_t n_rows;
+  __nv_bfloat16 *out;
+  int64_t out_ld;
+};
+// One work item: 128-row block (query or key), head, sequence.
+struct Item {
+  int blk, h, b, row0, T;
+};
+LLM_DEV Item pk_item(const PkView &pk, int item, int heads, bool keys) {
+  const int4 t = *reinterpret_cast<const int4 *>(pk.tiles + item / heads);
+  const int n = (t.y + PK_BLOCK - 1) / PK_BLOCK;
+  return Item{keys ? n - 1 - t.z : t.z, item % heads, 0, t.x, t.y};
+}
+// Rows [first, 32) of the 32-row group at `rows` (128-byte rows) to zero, by
+// the 128 threads of the group's four warps (t = 0 .. 127): the rows of a
+// tile past its sequence's end belong to another sequence or to none, and
+// 0 * NaN is NaN in a product.
+LLM_DEV void zero_rows(uint8_t *rows, int first, int t) {
+  if ((t >> 2) >= first) {
+    uint4 *p = reinterpret_cast<uint4 *>(rows + (t >> 2) * 128 + (t & 3) * 32);
+    p[0] = p[1] = make_uint4(0, 0, 0, 0);
+  }
+  tc::fence_proxy_async();
+}
+// The staged rows [r0, r0 + 8) of a 128-byte-swizzled tile that lie before
+// `end`, head columns [0, hd), to out (row r0 of the tile; row stride ld).
+LLM_DEV void store_cut(const uint8_t *tile, int r0, int end, __nv_bfloat16 *out, int64_t ld, int hd,
+                       int lane) {
+  const int r = r0 + (lane >> 2);
+  if (r >= end) return;
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    const int c = (lane & 3) + 4 * k;
+    if (c * 8 < hd)
+      *reinterpret_cast<uint4 *>(out + (int64_t)(lane >> 2) * ld + c * 8) =
+          *reinterpret_cast<const uint4 *>(tile + r * 128 + ((c ^ (r & 7)) << 4));
+  }
+}
 
 LLM_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -103,12 +149,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return encode;
 }
 
-// Loads: [rows][heads][hd] over a row-major [rows][ld] bf16 array (ld =
-// heads * hd), box 64 x 1 head x box_rows rows.
+// Loads: [rows][heads][hd] over a row-major [rows][ld] bf16 array (ld a
+// multiple of 8, at least heads * hd), box 64 x 1 head x box_rows rows.
 inline bool head_map_load(CUtensorMap *map, const void *base, int hd, int64_t heads, int64_t rows,
                           int64_t ld, int box_rows) {
   auto encode = encoder();
-  if (!encode || ((uintptr_t)base & 15) || (hd != 32 && hd != 64) || ld != heads * hd) return false;
+  if (!encode || ((uintptr_t)base & 15) || (hd != 32 && hd != 64) || ld < heads * hd || ld % 8)
+    return false;
   cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2};
   cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
@@ -119,12 +166,13 @@ inline bool head_map_load(CUtensorMap *map, const void *base, int hd, int64_t he
 }
 
 // Stores: [batches][T][heads][hd] over a row-major [batches * T][ld] bf16
-// array, box 64 x 1 head x box_rows rows x 1 batch (rows past T, and a
+// array (ld as above), box 64 x 1 head x box_rows rows x 1 batch (rows past T, and a
 // head-32 box's upper 32 values, are not written).
 inline bool head_map_store(CUtensorMap *map, void *base, int hd, int64_t heads, int64_t T,
                            int64_t batches, int64_t ld, int box_rows) {
   auto encode = encoder();
-  if (!encode || ((uintptr_t)base & 15) || (hd != 32 && hd != 64) || ld != heads * hd) return false;
+  if (!encode || ((uintptr_t)base & 15) || (hd != 32 && hd != 64) || ld < heads * hd || ld % 8)
+    return false;
   cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)batches};
   cuuint64_t strides[3] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2, (cuuint64_t)(ld * T * 2)};
   cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};

@@ -18,7 +18,7 @@ enum : int { PK_BAD_OFFSETS = 1, PK_BAD_PAGE = 2 };
 struct PkTile {
   int row0, len, blk, pad;
 };
-// The workspace: tile count, then the tiles (most work first), then scratch
+// The workspace: tile count (and a flag word for callers without one), then the tiles (most work first), then scratch
 // of the plan (clamped offsets, ranks), then D of the backward.
 struct PkPlan {
   int *n_tiles;
@@ -38,7 +38,7 @@ inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward)
     at = (at + n + 255) / 256 * 256;
     return q;
   };
-  p.n_tiles = (int *)take(4);
+  p.n_tiles = (int *)take(8);
   p.tiles = (PkTile *)take(p.cap * (int64_t)sizeof(PkTile));
   p.off = (int *)take(4 * ((int64_t)n_seq + 1));
   p.rank = (int *)take(4 * (int64_t)n_seq);
@@ -59,6 +59,11 @@ struct PkArgs {
   cudaStream_t s;
 };
 void packed_plan(const PkArgs &a, const PkPlan &p);
+// tcgen05 kernels: bfloat16, head sizes 32 and 64, rows that start on 16
+// bytes; false (nothing launched) otherwise.  flag: non-null device word.
+bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag);
+bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
+                   const void *dout, void *dqkv, int64_t dld, int *flag);
 // CUDA-core kernels: float32 arithmetic, either type, head sizes to 128.
 bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse);
 bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
