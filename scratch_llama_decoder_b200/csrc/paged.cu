@@ -1,6 +1,7 @@
 // The paged key/value cache: rows written (rounded or quantised) and read
 // back, and the attention of one new token per sequence over its cached
 // positions, split over their number and joined.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <limits.h>
 
@@ -490,6 +491,516 @@ __global__ void __launch_bounds__(AT)
   }
 }
 
+// ------------------------------------------- bfloat16 queries, tensor cores
+// The same work on mma.m16n8k16, the cached rows as the 16-row operand, so
+// that a kv head's query heads fill the 8 columns (NT column tiles) and no
+// row of a product is padding:
+//   S^T [16 keys x 8 heads]  = K [16 x HD] q^T       (HD / 16 steps)
+//   O^T [16 columns x 8] += V^T [16 x 16 keys] P^T   (HD / 16 tiles)
+// Nothing passes through shared memory: a lane reads its operands of K and V
+// from global memory in 16-byte (or row / 8) pieces, because the sums over
+// head columns (S) and over keys (O) may take them in any order: lane (g, t) =
+// (lane / 4, lane % 4) reads of key g a contiguous quarter of the row and
+// calls its columns k-step s those that the fragment wants, and of keys
+// 2t, 2t+1, 2t+8, 2t+9 an eighth of the row.  P^T comes from S^T's own
+// registers by transposing 8 x 8 blocks (movmatrix).  Each of the 4 warps
+// takes SB x 16 keys at a time with the next ones' loads in flight (K's issued
+// as soon as S is formed, V's after O), so the kernel needs no barrier until
+// the warps meet, and a block's latency is a few loads.
+// 8-bit caches: codes become float16 exactly (e4m3 and 8-bit integers both
+// fit); q is scaled per head by a power of two into [1, 2) so that it fits
+// float16's range; K's row scale multiplies the scores.  V's row scale cannot
+// be left to the products' end, so it joins the weight: with scale = f 2^e,
+// the weight 2^(s + e - mo) f uses a reference mo of its own (the running
+// maximum of s + e), which holds it within float16 whatever the scales are.
+// The bfloat16 and float16 rounding of the weights (2^-9 and 2^-12) is the
+// only rounding below 32 bits; the sum l takes them unrounded.
+constexpr int NW = AT / 32;
+// log2 units a maximum may grow before O is rescaled, and the log2 of a weight
+// at its reference: a float16 weight is at most 2^(13 + 1) f < 2^15, and those
+// below 2^-14 keep steps of 2^-24, 2^-37 of the reference
+template <bool BF> constexpr float LAZY = BF ? 8.f : 1.f;
+constexpr float OFF16 = 13.f;
+
+template <int W>
+LLM_DEV void ldg(const uint8_t *p, bool on, uint32_t (&r)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; i++) r[i] = 0;
+  if (on) {
+    if constexpr (W % 4 == 0) {
+      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+    } else if constexpr (W == 2) {
+      asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];"
+                   : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+    } else {
+      asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r[0]) : "l"(p));
+    }
+  }
+}
+template <bool BF>
+LLM_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                 uint32_t b1) {
+  if constexpr (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transposes the 8 x 8 matrix of 16-bit values the warp holds (row lane / 4,
+// columns 2 (lane % 4) and the next).
+LLM_DEV uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+template <bool BF>
+LLM_DEV uint32_t pack16(float lo, float hi) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+}
+LLM_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Codes in bytes (0, 1) of w, and (2, 3), as float16 pairs.
+template <int FMT>
+LLM_DEV void half_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if constexpr (FMT == KV_E4M3) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+        " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // byte + 128 as the low mantissa bits of 1024: 0x6400 | (c + 128) = 1152 + c
+    const uint32_t u = w ^ 0x80808080u, k = 0x64806480u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 kk = *reinterpret_cast<const __half2 *>(&k);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), kk);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), kk);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+  }
+}
+// Joins the warps' parts of one piece (m, l and O, in sm [NW][8 NT][HD + 2])
+// and writes the outputs, or the record of a cut pair: see k_attend.
+template <int HD, int HEADS>
+LLM_DEV void finish(const float *sm, int grp, int r0, int hd, bool whole, __nv_bfloat16 *o,
+                    float *lse, float *rec) {
+  for (int i = threadIdx.x; i < HEADS * HD; i += AT) {
+    const int r = i / HD, e = i % HD;
+    if (r0 + r >= grp) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < NW; x++) M = fmaxf(M, sm[(x * HEADS + r) * (HD + 2) + HD]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, v = 0.f;
+#pragma unroll
+    for (int x = 0; x < NW; x++) {
+      const float *w = sm + (x * HEADS + r) * (HD + 2);
+      const float f = exp2f(w[HD] - ref);
+      L = fmaf(f, w[HD + 1], L);
+      v = fmaf(f, w[e], v);
+    }
+    if (whole) {
+      o[(r0 + r) * hd + e] = from_f<__nv_bfloat16>(L == 0.f ? 0.f : v / L);
+      if (e == 0 && lse) lse[r0 + r] = (M + log2f(L)) * LN2;
+    } else {
+      rec[(r0 + r) * (hd + 2) + 2 + e] = v;
+      if (e == 0) {
+        rec[(r0 + r) * (hd + 2)] = M;
+        rec[(r0 + r) * (hd + 2) + 1] = L;
+      }
+    }
+  }
+}
+
+template <int FMT, int HD, int NT, int SB>
+__global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
+    k_attend_mma(const KvView kv, const __nv_bfloat16 *__restrict__ q, int64_t q_ld,
+                 const int32_t *__restrict__ lens, const Sched sc, int H,
+                 __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
+                 int *__restrict__ pre_out, float *__restrict__ part) {
+  constexpr bool BF = FMT == KV_BF16;
+  constexpr int ES = BF ? 2 : 1, KW = HD * ES / 16, VW = HD * ES / 32;  // words a lane and key
+  constexpr int KC = KW < 4 ? KW : 4, VC = VW < 4 ? VW : 4;            // words of one load
+  constexpr int KB = 16 * SB, GR = 2 * SB, WI = 32 / GR, HEADS = 8 * NT;
+  extern __shared__ int pre[];
+  __shared__ float sm[NW * HEADS * (HD + 2)];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lt = lane & 3;
+  const int grp = H / kv.Hkv;
+  const float sl2 = LOG2E / sqrtf((float)HD);
+  int64_t w = 0, end = 1;
+  if (!sc.direct) {
+    unit_prefix(kv, lens, sc.n_seq, pre);
+    if (blockIdx.x == 0)
+      for (int s = threadIdx.x; s <= sc.n_seq; s += AT) pre_out[s] = pre[s];
+    const int64_t W = (int64_t)pre[sc.n_seq] * kv.Hkv;
+    const int N = (int)min((int64_t)sc.N, W);
+    if ((int)blockIdx.x >= N) return;
+    w = block_begin(W, blockIdx.x, N);
+    end = block_begin(W, blockIdx.x + 1, N);
+  }
+  for (int piece = 0; w < end; piece++) {
+    int s, g, j0, j1;
+    bool whole = true;
+    if (sc.direct) {
+      s = blockIdx.x / kv.Hkv;
+      g = blockIdx.x % kv.Hkv;
+      j0 = 0;
+      j1 = clamped_len(kv, lens, s);
+      w = end;
+    } else {
+      s = seq_at(pre, sc.n_seq, w, kv.Hkv);
+      const int units = pre[s + 1] - pre[s];
+      const int64_t in = w - (int64_t)pre[s] * kv.Hkv;
+      g = (int)(in / units);
+      const int u0 = (int)(in - (int64_t)g * units);
+      const int nu = (int)min((int64_t)(units - u0), end - w);
+      w += nu;
+      whole = nu == units;
+      const int64_t cap = (int64_t)kv.table_pages * kv.ps;
+      j0 = u0 * PG_UNIT;
+      j1 = (int)min(min((int64_t)lens[s], cap), (int64_t)(u0 + nu) * PG_UNIT);
+    }
+    const int32_t *table = kv.table + (int64_t)s * kv.table_ld;
+    const int64_t vrows = (int64_t)kv.Hkv * kv.ps;  // from a key's row to its value's
+    const int nit = (j1 - j0 + NW * KB - 1) / (NW * KB);
+    for (int r0 = 0; r0 < grp; r0 += HEADS) {
+      // q^T fragments: head lg of each tile, columns as K's words hold them
+      uint32_t qf[NT][HD / 16][2];
+      float qs[NT][2];  // log2-score factor of this lane's heads 2 lt, 2 lt + 1
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const int hh = r0 + n * 8 + lg;
+        const __nv_bfloat16 *qr = q + s * q_ld + (int64_t)(g * grp + hh) * HD;
+        float x[HD / 16][4], top = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ks++) {
+          const int d = BF ? (ks / 2 * 4 + lt) * 8 + (ks & 1) * 4
+                           : KW == 2 ? lt * 8 + ks * 4 : (ks / 4 * 4 + lt) * 16 + (ks & 3) * 4;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            x[ks][i] = hh < grp ? to_f(qr[d + i]) : 0.f;
+            top = fmaxf(top, fabsf(x[ks][i]));
+          }
+        }
+        float up = 1.f, down = 1.f;
+        if constexpr (!BF) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = (int)(__float_as_uint(top) >> 23);  // top < 2^128: its exponent
+          if (e > 0 && e < 255) {  // up = 2^-(e - 127), within [2^-126, 2^126]
+            const int k = min(max(e - 127, -126), 126);
+            up = __uint_as_float((uint32_t)(127 - k) << 23);
+            down = __uint_as_float((uint32_t)(127 + k) << 23);
+          }
+        }
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ks++) {
+          qf[n][ks][0] = pack16<BF>(x[ks][0] * up, x[ks][1] * up);
+          qf[n][ks][1] = pack16<BF>(x[ks][2] * up, x[ks][3] * up);
+        }
+        // the factors of heads 2 lt and 2 lt + 1 sit in lanes of rows lg = those
+        qs[n][0] = sl2 * __shfl_sync(0xffffffffu, down, 8 * lt);
+        qs[n][1] = sl2 * __shfl_sync(0xffffffffu, down, 8 * lt + 4);
+      }
+      float acc[NT][HD / 16][4], m[NT][2], mo[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          m[n][c] = mo[n][c] = -INFINITY;
+          l[n][c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 16; i++)
+#pragma unroll
+          for (int c = 0; c < 4; c++) acc[n][i][c] = 0.f;
+      }
+      uint32_t kr[SB][2][KW], vr[SB][4][VW];
+      float kscale[SB][2], vscale[SB][2];
+      int win = -1;     // first row of 8-key group `lane` of the window, -1: none
+      uint32_t there = 0, there_next = 0;  // groups of the iteration whose page exists
+      // rows of a group of the iteration `it`: the window of 32 groups is
+      // looked up by the lanes, one division and table entry each
+      auto look_up = [&](int it) {
+        if (it % WI == 0) {
+          const int64_t key = j0 + ((int64_t)(it + lane / GR) * NW + warp) * KB + (lane % GR) * 8;
+          win = -1;
+          if (key < j1) {
+            const uint32_t pg = (uint32_t)key / (uint32_t)kv.ps;
+            const int64_t page = table[pg];
+            if (page >= 0 && page < kv.n_pages)
+              win = (int)(page * (2 * vrows)) + g * kv.ps + (int)((uint32_t)key - pg * kv.ps);
+            else if (kv.flag)
+              atomicOr(kv.flag, PK_BAD_PAGE);
+          }
+        }
+      };
+      auto load_k = [&](int it) {
+        look_up(it);
+        const int base = (it % WI) * GR;
+        there_next = 0;
+#pragma unroll
+        for (int b = 0; b < SB; b++)
+#pragma unroll
+          for (int hf = 0; hf < 2; hf++) {
+            const int row = __shfl_sync(0xffffffffu, win, base + 2 * b + hf);
+            const bool on = row >= 0;
+            there_next |= (uint32_t)on << (2 * b + hf);
+            const uint8_t *p = kv.pages + ((int64_t)row + lg) * (HD * ES) + lt * (KC * 4);
+#pragma unroll
+            for (int c = 0; c < KW / KC; c++) {
+              uint32_t t[KC];
+              ldg<KC>(p + c * 64, on, t);
+#pragma unroll
+              for (int i = 0; i < KC; i++) kr[b][hf][c * KC + i] = t[i];
+            }
+            if constexpr (!BF) kscale[b][hf] = on ? __ldg(kv.scales + row + lg) : 0.f;
+          }
+      };
+      auto load_v = [&](int it) {
+        const int base = (it % WI) * GR;
+        const int64_t key0 = j0 + ((int64_t)it * NW + warp) * KB;
+#pragma unroll
+        for (int b = 0; b < SB; b++)
+#pragma unroll
+          for (int hf = 0; hf < 2; hf++) {
+            const int row = __shfl_sync(0xffffffffu, win, base + 2 * b + hf);
+#pragma unroll
+            for (int k = 0; k < 2; k++) {  // keys 2 lt + k of the group: zeros past the end
+              const bool on = row >= 0 && key0 + 16 * b + 8 * hf + 2 * lt + k < j1;
+              const uint8_t *p = kv.pages + (row + vrows + 2 * lt + k) * (HD * ES) + lg * (VC * 4);
+#pragma unroll
+              for (int c = 0; c < VW / VC; c++) {
+                uint32_t t[VC];
+                ldg<VC>(p + c * 128, on, t);
+#pragma unroll
+                for (int i = 0; i < VC; i++) vr[b][2 * hf + k][c * VC + i] = t[i];
+              }
+            }
+            if constexpr (!BF)
+              vscale[b][hf] = row >= 0 && key0 + 16 * b + 8 * hf + lg < j1
+                                  ? __ldg(kv.scales + row + vrows + lg) : 0.f;
+          }
+      };
+      if (nit > 0) {
+        load_k(0);
+        load_v(0);
+        there = there_next;
+      }
+      for (int it = 0; it < nit; it++) {
+        const int64_t key0 = j0 + ((int64_t)it * NW + warp) * KB;
+        float st[NT][SB][4];
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int b = 0; b < SB; b++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) st[n][b][c] = 0.f;
+#pragma unroll
+        for (int b = 0; b < SB; b++)
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ks++) {
+            uint32_t a[4];
+            if constexpr (BF) {
+              a[0] = kr[b][0][2 * ks];
+              a[2] = kr[b][0][2 * ks + 1];
+              a[1] = kr[b][1][2 * ks];
+              a[3] = kr[b][1][2 * ks + 1];
+            } else {
+              half_pairs<FMT>(kr[b][0][ks], a[0], a[2]);
+              half_pairs<FMT>(kr[b][1][ks], a[1], a[3]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+              mma<BF>(st[n][b], a[0], a[1], a[2], a[3], qf[n][ks][0], qf[n][ks][1]);
+          }
+        float kc[SB][2];
+        if constexpr (!BF) {
+#pragma unroll
+          for (int b = 0; b < SB; b++) {
+            kc[b][0] = kscale[b][0];
+            kc[b][1] = kscale[b][1];
+          }
+        }
+        if (it + 1 < nit) load_k(it + 1);
+        // log2 scores; keys past the end or without a page: weight 0
+        const bool ragged = key0 + KB > j1 || there != (1u << GR) - 1;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int b = 0; b < SB; b++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              const int hf = c >> 1;
+              float x = st[n][b][c] * qs[n][c & 1];
+              if constexpr (!BF) x *= kc[b][hf];
+              if (ragged && (key0 + 16 * b + 8 * hf + lg >= j1 || !(there >> (2 * b + hf) & 1)))
+                x = -INFINITY;
+              st[n][b][c] = x;
+            }
+        // V's scale of keys lg and lg + 8 of each block as f 2^e
+        float vf[SB][2], ve[SB][2];
+        if constexpr (!BF) {
+#pragma unroll
+          for (int b = 0; b < SB; b++)
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+              const uint32_t u = __float_as_uint(vscale[b][hf]), ex = u >> 23 & 0xff;
+              const bool plain = ex > 0 && ex < 255;  // else 0, subnormal or not finite: f alone
+              ve[b][hf] = plain ? (float)((int)ex - 127) : 0.f;
+              vf[b][hf] = plain ? __uint_as_float((u & 0x807fffffu) | 0x3f800000u) : vscale[b][hf];
+            }
+        }
+        // a maximum that grew by more than that moves its reference (in every
+        // lane of the head: the lanes of its keys agree by shuffles)
+        bool grew = false;
+        float top[NT][2], topo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            float a = -INFINITY, z = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < SB; b++) {
+              a = fmaxf(a, fmaxf(st[n][b][c], st[n][b][2 + c]));
+              if constexpr (!BF)
+                z = fmaxf(z, fmaxf(st[n][b][c] + ve[b][0], st[n][b][2 + c] + ve[b][1]));
+            }
+            top[n][c] = a;
+            topo[n][c] = z;
+            grew |= a > m[n][c] + LAZY<BF>;
+            if constexpr (!BF) grew |= z > mo[n][c] + LAZY<BF>;
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+              float a = top[n][c], z = topo[n][c];
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) {
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, x));
+                if constexpr (!BF) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, x));
+              }
+              const float mn = fmaxf(m[n][c], a);
+              const float corr = mn == -INFINITY ? 1.f : ex2(m[n][c] - mn);
+              l[n][c] *= corr;
+              m[n][c] = mn;
+              float co = corr;
+              if constexpr (!BF) {
+                const float zn = fmaxf(mo[n][c], z);
+                co = zn == -INFINITY ? 1.f : ex2(mo[n][c] - zn);
+                mo[n][c] = zn;
+              }
+#pragma unroll
+              for (int i = 0; i < HD / 16; i++) {
+                acc[n][i][c] *= co;
+                acc[n][i][2 + c] *= co;
+              }
+            }
+        }
+        // weights and their B fragments
+        uint32_t pf[NT][SB][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          float ref[2], refo[2];
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            ref[c] = m[n][c] == -INFINITY ? 0.f : m[n][c];
+            refo[c] = (mo[n][c] == -INFINITY ? 0.f : mo[n][c]) - OFF16;
+          }
+#pragma unroll
+          for (int b = 0; b < SB; b++) {
+            float p[4];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+              p[c] = ex2(st[n][b][c] - ref[c & 1]);
+              l[n][c & 1] += p[c];
+              if constexpr (!BF)
+                p[c] = ex2(st[n][b][c] + ve[b][c >> 1] - refo[c & 1]) * vf[b][c >> 1];
+            }
+            pf[n][b][0] = transpose8(pack16<BF>(p[0], p[1]));
+            pf[n][b][1] = transpose8(pack16<BF>(p[2], p[3]));
+          }
+        }
+        // O^T += V^T P^T: tile i holds columns d and d + 1 of word i (bf16), or
+        // a pair of the four of a word of codes
+#pragma unroll
+        for (int b = 0; b < SB; b++) {
+#pragma unroll
+          for (int i = 0; i < VW; i++) {
+            if constexpr (BF) {
+              const uint32_t a0 = __byte_perm(vr[b][0][i], vr[b][1][i], 0x5410);
+              const uint32_t a1 = __byte_perm(vr[b][0][i], vr[b][1][i], 0x7632);
+              const uint32_t a2 = __byte_perm(vr[b][2][i], vr[b][3][i], 0x5410);
+              const uint32_t a3 = __byte_perm(vr[b][2][i], vr[b][3][i], 0x7632);
+#pragma unroll
+              for (int n = 0; n < NT; n++)
+                mma<BF>(acc[n][i], a0, a1, a2, a3, pf[n][b][0], pf[n][b][1]);
+            } else {
+              uint32_t x[4], y[4];  // columns 0 .. 3 of the word: keys 2t, 2t+1; 2t+8, 2t+9
+              half_pairs<FMT>(__byte_perm(vr[b][0][i], vr[b][1][i], 0x5140), x[0], x[1]);
+              half_pairs<FMT>(__byte_perm(vr[b][0][i], vr[b][1][i], 0x7362), x[2], x[3]);
+              half_pairs<FMT>(__byte_perm(vr[b][2][i], vr[b][3][i], 0x5140), y[0], y[1]);
+              half_pairs<FMT>(__byte_perm(vr[b][2][i], vr[b][3][i], 0x7362), y[2], y[3]);
+#pragma unroll
+              for (int n = 0; n < NT; n++) {
+                mma<BF>(acc[n][2 * i], x[0], x[1], y[0], y[1], pf[n][b][0], pf[n][b][1]);
+                mma<BF>(acc[n][2 * i + 1], x[2], x[3], y[2], y[3], pf[n][b][0], pf[n][b][1]);
+              }
+            }
+          }
+        }
+        if (it + 1 < nit) load_v(it + 1);
+        there = there_next;
+      }
+      // the warp's O, in units of its maximum, and its sums to shared memory
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], x);
+          float f = 1.f;
+          if constexpr (!BF) f = mo[n][c] == -INFINITY ? 1.f : exp2f(mo[n][c] - m[n][c] - OFF16);
+          float *dst = sm + (warp * HEADS + n * 8 + 2 * lt + c) * (HD + 2);
+#pragma unroll
+          for (int i = 0; i < HD / 16; i++) {
+            const int d = BF ? (VW == 2 ? lg * 4 + i * 2 : (i / 4 * 8 + lg) * 8 + (i & 3) * 2)
+                             : lg * (HD / 8) + i * 2;
+            dst[d] = acc[n][i][c] * f;
+            dst[d + 1] = acc[n][i][2 + c] * f;
+          }
+          if (lg == 0) {
+            dst[HD] = m[n][c];
+            dst[HD + 1] = l[n][c];
+          }
+        }
+      __syncthreads();
+      finish<HD, HEADS>(sm, grp, r0, HD, whole, o + ((int64_t)s * H + g * grp) * HD,
+                        lse ? lse + (int64_t)s * H + g * grp : nullptr,
+                        part + (int64_t)(2 * blockIdx.x + (piece > 0)) * grp * (HD + 2));
+      __syncthreads();
+    }
+  }
+}
+
 // Joins the parts of every cut pair, in order; a sequence of length 0 gets
 // o = 0 and L = -inf.
 template <typename T>
@@ -546,6 +1057,43 @@ static bool attend(const PagedArgs &a, const Sched &sc, int *pre, float *part, b
     count_launch();
   }
   return true;
+}
+template <int FMT, int HD, int NT, int SB>
+static bool attend_mma(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
+  using T = __nv_bfloat16;
+  auto kern = k_attend_mma<FMT, HD, NT, SB>;
+  if (!smem_optin((const void *)kern, 4 * (PG_MAX_SEQ + 1))) return false;
+  kern<<<sc.N, AT, sc.direct ? 0 : 4 * (a.n_seq + 1), a.s>>>(
+      a.kv, (const T *)a.q, a.q_ld, a.lens, sc, a.H, (T *)a.o, a.lse, pre, part);
+  count_launch();
+  if (!sc.direct) {
+    k_join<T><<<a.n_seq * a.kv.Hkv, AT, 0, a.s>>>(pre, part, sc, a.H, a.kv.hd, (T *)a.o, a.lse);
+    count_launch();
+  }
+  return true;
+}
+template <int FMT, int HD, int SB>
+static bool attend_mma_nt(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
+  return a.H / a.kv.Hkv <= 8 ? attend_mma<FMT, HD, 1, SB>(a, sc, pre, part)
+                             : attend_mma<FMT, HD, 2, SB>(a, sc, pre, part);
+}
+template <int FMT>
+static bool attend_mma_hd(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
+  constexpr int SB = 2;
+  switch (a.kv.hd) {
+    case 32: return attend_mma_nt<FMT, 32, SB>(a, sc, pre, part);
+    case 64: return attend_mma_nt<FMT, 64, SB>(a, sc, pre, part);
+    default: return attend_mma_nt<FMT, 128, FMT == KV_BF16 ? 1 : SB>(a, sc, pre, part);
+  }
+}
+// The tensor-core kernels: bfloat16 queries over a bfloat16 or 8-bit cache,
+// head sizes 32, 64 and 128, pages of a multiple of 8 rows (8 consecutive
+// positions lie in one page), 16-byte aligned, row numbers within 31 bits.
+static bool mma_covers(const PagedArgs &a) {
+  const KvView &kv = a.kv;
+  return a.dt == DT_BF16 && kv.fmt != KV_F32 && (kv.hd == 32 || kv.hd == 64 || kv.hd == 128) &&
+         kv.ps % 8 == 0 && !((uintptr_t)kv.pages & 15) &&
+         kv.n_pages < ((int64_t)1 << 31) / (2 * (int64_t)kv.Hkv * kv.ps);
 }
 template <typename T, int FMT>
 static bool attend_hd(const PagedArgs &a, const Sched &sc, int *pre, float *part, bool vec) {
@@ -626,6 +1174,13 @@ bool paged_attention(const PagedArgs &a) {
   const Sched sc = schedule(a.kv, a.n_seq);
   int *pre = (int *)a.ws;
   float *part = (float *)((uint8_t *)a.ws + pre_bytes(a.n_seq));
+  if (mma_covers(a)) {
+    switch (a.kv.fmt) {
+      case KV_BF16: return attend_mma_hd<KV_BF16>(a, sc, pre, part);
+      case KV_E4M3: return attend_mma_hd<KV_E4M3>(a, sc, pre, part);
+      default: return attend_mma_hd<KV_INT8>(a, sc, pre, part);
+    }
+  }
   const bool vec = a.kv.hd % 8 == 0 && !((uintptr_t)a.kv.pages & 15);
   return a.dt == DT_BF16 ? attend_fmt<__nv_bfloat16>(a, sc, pre, part, vec)
                          : attend_fmt<float>(a, sc, pre, part, vec);

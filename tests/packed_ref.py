@@ -137,7 +137,14 @@ def stored(x, fmt):
 
 def paged(q, pages, scales, table, lens, h, want):
     """out, lse and bounds of one token per sequence over its cached rows;
-    positions whose page is outside the cache are left out."""
+    positions whose page is outside the cache are left out.
+
+    bfloat16 queries over an 8-bit cache: a key's weight times its v scale may
+    be held in float16 (the codes fit it exactly), in units where the largest
+    so far is 2^13 at least, of which 2^-25 is half the least step: each key is
+    off by 2^-38 max_j(p_j scale_j) |code| at most beside the relative error,
+    which matters where every weight but one is far below 2^-14 of the largest
+    and that one's code is 0."""
     n_pages, _, g, ps, hd = pages.shape
     b = q.shape[0]
     x = pages.double() if scales is None else pages.double() * scales.double()[..., None]
@@ -166,5 +173,9 @@ def paged(q, pages, scales, table, lens, h, want):
                         + 3 * U * sc.abs()).max())
             ob[s, i] = (2 * (es + ex) + (2 * m + 16) * U + r) * (p @ v.abs()) + \
                 R[want] * out[s, i].abs()
+            if scales is not None and want == torch.bfloat16:
+                sv = scales[pi, 1, i // (h // g), ti].double()
+                codes = pages[pi, 1, i // (h // g), ti].double().abs().sum(0)
+                ob[s, i] += 2.0 ** -38 * float((p * sv).max()) * codes
             lb[s, i] = es + ex + (m + 8) * U + 4 * U * lse[s, i].abs()
     return out.reshape(b, -1), lse, ob.reshape(b, -1) + 1e-30, lb + 1e-30
