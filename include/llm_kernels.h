@@ -223,7 +223,8 @@ int llm_kernel_kv_read(const llm_kv *kv, const int32_t *d_cu, const int32_t *d_s
  * without a place as not there (d_flag of the cache, LLM_KV_BAD_PAGE).  What
  * the pages hold past a sequence's length is not looked at.  d_ws: at least
  * llm_kernel_attention_paged_workspace() bytes, 16-byte aligned, no
- * initialisation needed, one per call that may overlap another on the GPU.
+ * initialisation needed, one per call that may overlap another on the GPU (not
+ * looked at when that is 0: short tables, whose sequences are not split).
  * The lengths are read on the device: a captured call serves any.  The work is
  * split over the cached positions whatever the lengths are, and joined in a
  * fixed order: the same inputs give the same bits.  n_seq <= 8192. */

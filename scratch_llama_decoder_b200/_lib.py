@@ -73,7 +73,7 @@ class llm_kv(C.Structure):
 
 _vp, _i64, _u64, _f, _i = C.c_void_p, C.c_int64, C.c_uint64, C.c_float, C.c_int
 _cfgp = C.POINTER(llm_config)
-_kvp = C.POINTER(llm_kv)
+_kvp = _vp  # a reference to an llm_kv, or its bytes
 
 EXPORTS = {
     "llm_param_layout": (_i, [_cfgp, C.POINTER(llm_tensor_info), C.POINTER(_i), C.POINTER(_i64)]),

@@ -167,9 +167,10 @@ int llm_kernel_attention_paged(const llm_kv *kv, const void *d_q, int64_t q_ld, 
     return LLM_ERR_ARG;
   if (n_seq == 0) return LLM_OK;
   if (!aligned(d_q, elem(dtype)) || !aligned(d_lens, 4) || !aligned(d_o, elem(dtype)) ||
-      (d_lse && !aligned(d_lse, 4)) || !aligned(d_ws, 16) ||
-      ws_bytes < paged_ws_bytes(a.kv, n_seq, n_head))
+      (d_lse && !aligned(d_lse, 4)))
     return LLM_ERR_ARG;
+  const int64_t need = paged_ws_bytes(a.kv, n_seq, n_head);
+  if (need > 0 && (!aligned(d_ws, 16) || ws_bytes < need)) return LLM_ERR_ARG;
   if (!claim_device(nullptr)) return LLM_ERR_ARG;
   g_launches = 0;
   a.q = d_q;

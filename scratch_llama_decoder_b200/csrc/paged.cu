@@ -1165,7 +1165,7 @@ void kv_read(const KvView &kv, const int32_t *cu, const int32_t *start, int n_se
 
 int64_t paged_ws_bytes(const KvView &kv, int n_seq, int H) {
   const pg::Sched sc = pg::schedule(kv, n_seq);
-  if (sc.direct) return 256;
+  if (sc.direct) return 0;
   return pg::pre_bytes(n_seq) + 4 * 2 * (int64_t)sc.N * (H / kv.Hkv) * (kv.hd + 2);
 }
 

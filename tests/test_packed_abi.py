@@ -54,7 +54,7 @@ def test_packed_refusals():
 
 
 def _kv(P, **kw):
-    a = dict(d_pages=X, d_scales=X, d_table=X, table_ld=4, n_pages=10, table_pages=4, format=3,
+    a = dict(d_pages=X, d_scales=X, d_table=X, table_ld=400, n_pages=10, table_pages=400, format=3,
              n_kv_head=2, head_dim=64, page_size=16, d_flag=None)
     a.update(kw)
     return P._lib.llm_kv(**a)
