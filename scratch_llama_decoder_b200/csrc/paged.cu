@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <limits.h>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -506,36 +507,37 @@ __global__ void __launch_bounds__(AT)
 // registers by transposing 8 x 8 blocks (movmatrix).  Each of the 4 warps
 // takes SB x 16 keys at a time with the next ones' loads in flight (K's issued
 // as soon as S is formed, V's after O), so the kernel needs no barrier until
-// the warps meet, and a block's latency is a few loads.
+// the warps meet, and a block's latency is a few loads.  BIG: the SB x 16
+// positions lie in one page (page sizes of a multiple of SB x 16), so one
+// table entry and one address serve them; else each 8 positions have their
+// own.  GC: query heads a lane holds of a column tile, 1 when the kv head has
+// one query head (its second column, as the other lanes', is padding).
 // 8-bit caches: codes become float16 exactly (e4m3 and 8-bit integers both
 // fit); q is scaled per head by a power of two into [1, 2) so that it fits
 // float16's range; K's row scale multiplies the scores.  V's row scale cannot
-// be left to the products' end, so it joins the weight: with scale = f 2^e,
-// the weight 2^(s + e - mo) f uses a reference mo of its own (the running
-// maximum of s + e), which holds it within float16 whatever the scales are.
+// be left to the products' end, so it joins the weight: 2^(s + log2 scale -
+// mo), whose reference mo of its own (the running maximum of s + log2 scale)
+// holds it within float16 whatever the scales are.
 // The bfloat16 and float16 rounding of the weights (2^-9 and 2^-12) is the
 // only rounding below 32 bits; the sum l takes them unrounded.
 constexpr int NW = AT / 32;
 // log2 units a maximum may grow before O is rescaled, and the log2 of a weight
-// at its reference: a float16 weight is at most 2^(13 + 1) f < 2^15, and those
-// below 2^-14 keep steps of 2^-24, 2^-37 of the reference
+// at its reference: a float16 weight is at most 2^(14 + 1), and those below
+// 2^-14 keep steps of 2^-24, 2^-38 of the reference
 template <bool BF> constexpr float LAZY = BF ? 8.f : 1.f;
-constexpr float OFF16 = 13.f;
+constexpr float OFF16 = 14.f;
 
+// W consecutive 32-bit words, read once.
 template <int W>
-LLM_DEV void ldg(const uint8_t *p, bool on, uint32_t (&r)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; i++) r[i] = 0;
-  if (on) {
-    if constexpr (W % 4 == 0) {
-      asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
-    } else if constexpr (W == 2) {
-      asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];"
-                   : "=r"(r[0]), "=r"(r[1]) : "l"(p));
-    } else {
-      asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r[0]) : "l"(p));
-    }
+LLM_DEV void ldg(const uint8_t *p, uint32_t *r) {
+  if constexpr (W % 4 == 0) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+  } else if constexpr (W == 2) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+  } else {
+    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r[0]) : "l"(p));
   }
 }
 template <bool BF>
@@ -574,6 +576,11 @@ LLM_DEV uint32_t pack16(float lo, float hi) {
 LLM_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+LLM_DEV float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // Codes in bytes (0, 1) of w, and (2, 3), as float16 pairs.
@@ -628,7 +635,7 @@ LLM_DEV void finish(const float *sm, int grp, int r0, int hd, bool whole, __nv_b
   }
 }
 
-template <int FMT, int HD, int NT, int SB>
+template <int FMT, int HD, int NT, int SB, int GC, bool BIG>
 __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
     k_attend_mma(const KvView kv, const __nv_bfloat16 *__restrict__ q, int64_t q_ld,
                  const int32_t *__restrict__ lens, const Sched sc, int H,
@@ -637,7 +644,8 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
   constexpr bool BF = FMT == KV_BF16;
   constexpr int ES = BF ? 2 : 1, KW = HD * ES / 16, VW = HD * ES / 32;  // words a lane and key
   constexpr int KC = KW < 4 ? KW : 4, VC = VW < 4 ? VW : 4;            // words of one load
-  constexpr int KB = 16 * SB, GR = 2 * SB, WI = 32 / GR, HEADS = 8 * NT;
+  constexpr int KB = 16 * SB, GR = BIG ? 1 : 2 * SB, WI = 32 / GR, HEADS = 8 * NT;
+  constexpr uint32_t ALL = (1u << GR) - 1;
   extern __shared__ int pre[];
   __shared__ float sm[NW * HEADS * (HD + 2)];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lt = lane & 3;
@@ -718,11 +726,11 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
         qs[n][0] = sl2 * __shfl_sync(0xffffffffu, down, 8 * lt);
         qs[n][1] = sl2 * __shfl_sync(0xffffffffu, down, 8 * lt + 4);
       }
-      float acc[NT][HD / 16][4], m[NT][2], mo[NT][2], l[NT][2];
+      float acc[NT][HD / 16][4], m[NT][GC], mo[NT][GC], l[NT][GC];
 #pragma unroll
       for (int n = 0; n < NT; n++) {
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
+        for (int c = 0; c < GC; c++) {
           m[n][c] = mo[n][c] = -INFINITY;
           l[n][c] = 0.f;
         }
@@ -733,13 +741,15 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
       }
       uint32_t kr[SB][2][KW], vr[SB][4][VW];
       float kscale[SB][2], vscale[SB][2];
-      int win = -1;     // first row of 8-key group `lane` of the window, -1: none
+      // the window: first row of the positions that lane i looked up (group
+      // i % GR of iteration i / GR from the window's first on), -1 for none
+      int win = -1;
       uint32_t there = 0, there_next = 0;  // groups of the iteration whose page exists
-      // rows of a group of the iteration `it`: the window of 32 groups is
-      // looked up by the lanes, one division and table entry each
+      bool full = false, full_next = false;  // every position counts
       auto look_up = [&](int it) {
         if (it % WI == 0) {
-          const int64_t key = j0 + ((int64_t)(it + lane / GR) * NW + warp) * KB + (lane % GR) * 8;
+          const int64_t key =
+              j0 + ((int64_t)(it + lane / GR) * NW + warp) * KB + (lane % GR) * (KB / GR);
           win = -1;
           if (key < j1) {
             const uint32_t pg = (uint32_t)key / (uint32_t)kv.ps;
@@ -751,60 +761,80 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
           }
         }
       };
+      const uint8_t *klane = kv.pages + lg * (HD * ES) + lt * (KC * 4);
+      const uint8_t *vlane = kv.pages + (vrows + 2 * lt) * (HD * ES) + lg * (VC * 4);
+      const float *slane = kv.scales + lg;
       auto load_k = [&](int it) {
         look_up(it);
-        const int base = (it % WI) * GR;
+        const int64_t key0 = j0 + ((int64_t)it * NW + warp) * KB;
         there_next = 0;
+        int row[GR];
+#pragma unroll
+        for (int i = 0; i < GR; i++) {
+          row[i] = __shfl_sync(0xffffffffu, win, (it % WI) * GR + i);
+          there_next |= (uint32_t)(row[i] >= 0) << i;
+        }
+        full_next = there_next == ALL && key0 + KB <= j1;
 #pragma unroll
         for (int b = 0; b < SB; b++)
 #pragma unroll
           for (int hf = 0; hf < 2; hf++) {
-            const int row = __shfl_sync(0xffffffffu, win, base + 2 * b + hf);
-            const bool on = row >= 0;
-            there_next |= (uint32_t)on << (2 * b + hf);
-            const uint8_t *p = kv.pages + ((int64_t)row + lg) * (HD * ES) + lt * (KC * 4);
+            // BIG: positions in one page, consecutive rows
+            const int64_t r = BIG ? (int64_t)row[0] + 16 * b + 8 * hf : row[(2 * b + hf) % GR];
+            const bool on = full_next || (BIG ? there_next != 0 : r >= 0);
+            if (on) {
 #pragma unroll
-            for (int c = 0; c < KW / KC; c++) {
-              uint32_t t[KC];
-              ldg<KC>(p + c * 64, on, t);
+              for (int c = 0; c < KW / KC; c++) ldg<KC>(klane + r * (HD * ES) + c * 64, &kr[b][hf][c * KC]);
+              if constexpr (!BF) kscale[b][hf] = __ldg(slane + r);
+            } else {
 #pragma unroll
-              for (int i = 0; i < KC; i++) kr[b][hf][c * KC + i] = t[i];
+              for (int i = 0; i < KW; i++) kr[b][hf][i] = 0;
+              kscale[b][hf] = 0.f;
             }
-            if constexpr (!BF) kscale[b][hf] = on ? __ldg(kv.scales + row + lg) : 0.f;
           }
       };
       auto load_v = [&](int it) {
-        const int base = (it % WI) * GR;
         const int64_t key0 = j0 + ((int64_t)it * NW + warp) * KB;
+        int row[GR];
+#pragma unroll
+        for (int i = 0; i < GR; i++) row[i] = __shfl_sync(0xffffffffu, win, (it % WI) * GR + i);
 #pragma unroll
         for (int b = 0; b < SB; b++)
 #pragma unroll
           for (int hf = 0; hf < 2; hf++) {
-            const int row = __shfl_sync(0xffffffffu, win, base + 2 * b + hf);
+            const int64_t r = BIG ? (int64_t)row[0] + 16 * b + 8 * hf : row[(2 * b + hf) % GR];
+            const uint8_t *p = vlane + r * (HD * ES);
+            const int64_t key = key0 + 16 * b + 8 * hf;
+            if (full_next) {
 #pragma unroll
-            for (int k = 0; k < 2; k++) {  // keys 2 lt + k of the group: zeros past the end
-              const bool on = row >= 0 && key0 + 16 * b + 8 * hf + 2 * lt + k < j1;
-              const uint8_t *p = kv.pages + (row + vrows + 2 * lt + k) * (HD * ES) + lg * (VC * 4);
+              for (int k = 0; k < 2; k++)
 #pragma unroll
-              for (int c = 0; c < VW / VC; c++) {
-                uint32_t t[VC];
-                ldg<VC>(p + c * 128, on, t);
+                for (int c = 0; c < VW / VC; c++)
+                  ldg<VC>(p + k * (HD * ES) + c * 128, &vr[b][2 * hf + k][c * VC]);
+              if constexpr (!BF) vscale[b][hf] = __ldg(slane + r + vrows);
+            } else {  // zeros where no position counts: 0 weights meet numbers
+              const bool page = BIG ? there_next != 0 : r >= 0;
 #pragma unroll
-                for (int i = 0; i < VC; i++) vr[b][2 * hf + k][c * VC + i] = t[i];
+              for (int k = 0; k < 2; k++) {
+#pragma unroll
+                for (int i = 0; i < VW; i++) vr[b][2 * hf + k][i] = 0;
+                if (page && key + 2 * lt + k < j1)
+#pragma unroll
+                  for (int c = 0; c < VW / VC; c++)
+                    ldg<VC>(p + k * (HD * ES) + c * 128, &vr[b][2 * hf + k][c * VC]);
               }
+              if constexpr (!BF)
+                vscale[b][hf] = page && key + lg < j1 ? __ldg(slane + r + vrows) : 0.f;
             }
-            if constexpr (!BF)
-              vscale[b][hf] = row >= 0 && key0 + 16 * b + 8 * hf + lg < j1
-                                  ? __ldg(kv.scales + row + vrows + lg) : 0.f;
           }
       };
       if (nit > 0) {
         load_k(0);
         load_v(0);
         there = there_next;
+        full = full_next;
       }
       for (int it = 0; it < nit; it++) {
-        const int64_t key0 = j0 + ((int64_t)it * NW + warp) * KB;
         float st[NT][SB][4];
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -830,58 +860,50 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
             for (int n = 0; n < NT; n++)
               mma<BF>(st[n][b], a[0], a[1], a[2], a[3], qf[n][ks][0], qf[n][ks][1]);
           }
-        float kc[SB][2];
-        if constexpr (!BF) {
+        // log2 scores x[n][b][hf][c] of keys 16 b + 8 hf + lg, heads 2 lt + c
+        float x[NT][SB][2][GC], lv[SB][2];
 #pragma unroll
-          for (int b = 0; b < SB; b++) {
-            kc[b][0] = kscale[b][0];
-            kc[b][1] = kscale[b][1];
+        for (int b = 0; b < SB; b++)
+#pragma unroll
+          for (int hf = 0; hf < 2; hf++) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+              for (int c = 0; c < GC; c++)
+                x[n][b][hf][c] = st[n][b][2 * hf + c] * (BF ? qs[n][c] : qs[n][c] * kscale[b][hf]);
+            lv[b][hf] = BF ? 0.f : lg2(vscale[b][hf]);
           }
+        if (!full) {  // keys past the end or without a page: weight 0
+          const int64_t key0 = j0 + ((int64_t)it * NW + warp) * KB;
+#pragma unroll
+          for (int b = 0; b < SB; b++)
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++)
+              if (key0 + 16 * b + 8 * hf + lg >= j1 || !(there >> (BIG ? 0 : 2 * b + hf) & 1)) {
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                  for (int c = 0; c < GC; c++) x[n][b][hf][c] = -INFINITY;
+                lv[b][hf] = 0.f;
+              }
         }
         if (it + 1 < nit) load_k(it + 1);
-        // log2 scores; keys past the end or without a page: weight 0
-        const bool ragged = key0 + KB > j1 || there != (1u << GR) - 1;
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-          for (int b = 0; b < SB; b++)
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-              const int hf = c >> 1;
-              float x = st[n][b][c] * qs[n][c & 1];
-              if constexpr (!BF) x *= kc[b][hf];
-              if (ragged && (key0 + 16 * b + 8 * hf + lg >= j1 || !(there >> (2 * b + hf) & 1)))
-                x = -INFINITY;
-              st[n][b][c] = x;
-            }
-        // V's scale of keys lg and lg + 8 of each block as f 2^e
-        float vf[SB][2], ve[SB][2];
-        if constexpr (!BF) {
-#pragma unroll
-          for (int b = 0; b < SB; b++)
-#pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-              const uint32_t u = __float_as_uint(vscale[b][hf]), ex = u >> 23 & 0xff;
-              const bool plain = ex > 0 && ex < 255;  // else 0, subnormal or not finite: f alone
-              ve[b][hf] = plain ? (float)((int)ex - 127) : 0.f;
-              vf[b][hf] = plain ? __uint_as_float((u & 0x807fffffu) | 0x3f800000u) : vscale[b][hf];
-            }
-        }
         // a maximum that grew by more than that moves its reference (in every
         // lane of the head: the lanes of its keys agree by shuffles)
         bool grew = false;
-        float top[NT][2], topo[NT][2];
+        float top[NT][GC], topo[NT][GC];
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-          for (int c = 0; c < 2; c++) {
+          for (int c = 0; c < GC; c++) {
             float a = -INFINITY, z = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < SB; b++) {
-              a = fmaxf(a, fmaxf(st[n][b][c], st[n][b][2 + c]));
-              if constexpr (!BF)
-                z = fmaxf(z, fmaxf(st[n][b][c] + ve[b][0], st[n][b][2 + c] + ve[b][1]));
-            }
+            for (int b = 0; b < SB; b++)
+#pragma unroll
+              for (int hf = 0; hf < 2; hf++) {
+                a = fmaxf(a, x[n][b][hf][c]);
+                if constexpr (!BF) z = fmaxf(z, x[n][b][hf][c] + lv[b][hf]);
+              }
             top[n][c] = a;
             topo[n][c] = z;
             grew |= a > m[n][c] + LAZY<BF>;
@@ -891,12 +913,12 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
 #pragma unroll
           for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
+            for (int c = 0; c < GC; c++) {
               float a = top[n][c], z = topo[n][c];
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) {
-                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, x));
-                if constexpr (!BF) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, x));
+              for (int o = 4; o < 32; o <<= 1) {
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                if constexpr (!BF) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
               }
               const float mn = fmaxf(m[n][c], a);
               const float corr = mn == -INFINITY ? 1.f : ex2(m[n][c] - mn);
@@ -919,25 +941,25 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
         uint32_t pf[NT][SB][2];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-          float ref[2], refo[2];
+          float ref[GC], refo[GC];
 #pragma unroll
-          for (int c = 0; c < 2; c++) {
+          for (int c = 0; c < GC; c++) {
             ref[c] = m[n][c] == -INFINITY ? 0.f : m[n][c];
             refo[c] = (mo[n][c] == -INFINITY ? 0.f : mo[n][c]) - OFF16;
           }
 #pragma unroll
-          for (int b = 0; b < SB; b++) {
-            float p[4];
+          for (int b = 0; b < SB; b++)
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-              p[c] = ex2(st[n][b][c] - ref[c & 1]);
-              l[n][c & 1] += p[c];
-              if constexpr (!BF)
-                p[c] = ex2(st[n][b][c] + ve[b][c >> 1] - refo[c & 1]) * vf[b][c >> 1];
+            for (int hf = 0; hf < 2; hf++) {
+              float p[2] = {0.f, 0.f};
+#pragma unroll
+              for (int c = 0; c < GC; c++) {
+                p[c] = ex2(x[n][b][hf][c] - ref[c]);
+                l[n][c] += p[c];
+                if constexpr (!BF) p[c] = ex2(x[n][b][hf][c] + (lv[b][hf] - refo[c]));
+              }
+              pf[n][b][hf] = transpose8(pack16<BF>(p[0], p[1]));
             }
-            pf[n][b][0] = transpose8(pack16<BF>(p[0], p[1]));
-            pf[n][b][1] = transpose8(pack16<BF>(p[2], p[3]));
-          }
         }
         // O^T += V^T P^T: tile i holds columns d and d + 1 of word i (bf16), or
         // a pair of the four of a word of codes
@@ -954,27 +976,28 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
               for (int n = 0; n < NT; n++)
                 mma<BF>(acc[n][i], a0, a1, a2, a3, pf[n][b][0], pf[n][b][1]);
             } else {
-              uint32_t x[4], y[4];  // columns 0 .. 3 of the word: keys 2t, 2t+1; 2t+8, 2t+9
-              half_pairs<FMT>(__byte_perm(vr[b][0][i], vr[b][1][i], 0x5140), x[0], x[1]);
-              half_pairs<FMT>(__byte_perm(vr[b][0][i], vr[b][1][i], 0x7362), x[2], x[3]);
-              half_pairs<FMT>(__byte_perm(vr[b][2][i], vr[b][3][i], 0x5140), y[0], y[1]);
-              half_pairs<FMT>(__byte_perm(vr[b][2][i], vr[b][3][i], 0x7362), y[2], y[3]);
+              uint32_t u[4], w[4];  // columns 0 .. 3 of the word: keys 2t, 2t+1; 2t+8, 2t+9
+              half_pairs<FMT>(__byte_perm(vr[b][0][i], vr[b][1][i], 0x5140), u[0], u[1]);
+              half_pairs<FMT>(__byte_perm(vr[b][0][i], vr[b][1][i], 0x7362), u[2], u[3]);
+              half_pairs<FMT>(__byte_perm(vr[b][2][i], vr[b][3][i], 0x5140), w[0], w[1]);
+              half_pairs<FMT>(__byte_perm(vr[b][2][i], vr[b][3][i], 0x7362), w[2], w[3]);
 #pragma unroll
               for (int n = 0; n < NT; n++) {
-                mma<BF>(acc[n][2 * i], x[0], x[1], y[0], y[1], pf[n][b][0], pf[n][b][1]);
-                mma<BF>(acc[n][2 * i + 1], x[2], x[3], y[2], y[3], pf[n][b][0], pf[n][b][1]);
+                mma<BF>(acc[n][2 * i], u[0], u[1], w[0], w[1], pf[n][b][0], pf[n][b][1]);
+                mma<BF>(acc[n][2 * i + 1], u[2], u[3], w[2], w[3], pf[n][b][0], pf[n][b][1]);
               }
             }
           }
         }
         if (it + 1 < nit) load_v(it + 1);
         there = there_next;
+        full = full_next;
       }
       // the warp's O, in units of its maximum, and its sums to shared memory
 #pragma unroll
       for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
+        for (int c = 0; c < GC; c++) {
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], x);
           float f = 1.f;
@@ -1025,18 +1048,37 @@ __global__ void __launch_bounds__(AT)
   // begins the block's range; in every later block it begins the range
   const int first = block_begin(W, b0, N) < w0 ? 1 : 0;
   const int64_t step = (int64_t)grp * (hd + 2);
+  constexpr int U = 8;  // parts whose loads are in flight together
   for (int i = threadIdx.x; i < grp * hd; i += AT) {
     const int r = i / hd, e = i % hd;
     float M = -INFINITY, L = 0.f, v = 0.f;
-    for (int b = b0; b <= b1; b++) {
-      const float *rec = part + (2 * b + (b == b0 ? first : 0)) * step + r * (hd + 2);
-      const float mn = fmaxf(M, rec[0]), ref = mn == -INFINITY ? 0.f : mn;
-      const float a = exp2f(M - ref), f = exp2f(rec[0] - ref);
-      L = L * a + rec[1] * f;
-      v = v * a + rec[2 + e] * f;
+    for (int b = b0; b <= b1; b += U) {
+      float pm[U], pl[U], pv[U], mn = M;
+#pragma unroll
+      for (int k = 0; k < U; k++) {
+        const bool in = b + k <= b1;
+        const float *rec = part + (2 * (in ? b + k : b0) + (b + k == b0 || !in ? first : 0)) * step +
+                           r * (hd + 2);
+        pm[k] = in ? __ldcg(rec) : -INFINITY;
+        pl[k] = __ldcg(rec + 1);
+        pv[k] = __ldcg(rec + 2 + e);
+      }
+#pragma unroll
+      for (int k = 0; k < U; k++) mn = fmaxf(mn, pm[k]);
+      const float ref = mn == -INFINITY ? 0.f : mn, a = exp2f(M - ref);
+      L *= a;
+      v *= a;
+#pragma unroll
+      for (int k = 0; k < U; k++) {
+        const float f = exp2f(pm[k] - ref);
+        if (b + k <= b1) {
+          L = fmaf(f, pl[k], L);
+          v = fmaf(f, pv[k], v);
+        }
+      }
       M = mn;
     }
-    o[((int64_t)s * H + g * grp + r) * hd + e] = from_f<T>(L == 0.f ? 0.f : v / L);
+    o[((int64_t)s * H + g * grp) * hd + i] = from_f<T>(L == 0.f ? 0.f : v / L);
     if (e == 0 && lse) lse[(int64_t)s * H + g * grp + r] = (M + log2f(L)) * LN2;
   }
 }
@@ -1058,10 +1100,10 @@ static bool attend(const PagedArgs &a, const Sched &sc, int *pre, float *part, b
   }
   return true;
 }
-template <int FMT, int HD, int NT, int SB>
+template <int FMT, int HD, int NT, int SB, int GC, bool BIG>
 static bool attend_mma(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
   using T = __nv_bfloat16;
-  auto kern = k_attend_mma<FMT, HD, NT, SB>;
+  auto kern = k_attend_mma<FMT, HD, NT, SB, GC, BIG>;
   if (!smem_optin((const void *)kern, 4 * (PG_MAX_SEQ + 1))) return false;
   kern<<<sc.N, AT, sc.direct ? 0 : 4 * (a.n_seq + 1), a.s>>>(
       a.kv, (const T *)a.q, a.q_ld, a.lens, sc, a.H, (T *)a.o, a.lse, pre, part);
@@ -1074,8 +1116,14 @@ static bool attend_mma(const PagedArgs &a, const Sched &sc, int *pre, float *par
 }
 template <int FMT, int HD, int SB>
 static bool attend_mma_nt(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
-  return a.H / a.kv.Hkv <= 8 ? attend_mma<FMT, HD, 1, SB>(a, sc, pre, part)
-                             : attend_mma<FMT, HD, 2, SB>(a, sc, pre, part);
+  const int grp = a.H / a.kv.Hkv;
+  auto go = [&](auto big) {
+    constexpr bool B = decltype(big)::value;
+    return grp == 1   ? attend_mma<FMT, HD, 1, SB, 1, B>(a, sc, pre, part)
+           : grp <= 8 ? attend_mma<FMT, HD, 1, SB, 2, B>(a, sc, pre, part)
+                      : attend_mma<FMT, HD, 2, SB, 2, B>(a, sc, pre, part);
+  };
+  return a.kv.ps % (16 * SB) == 0 ? go(std::true_type()) : go(std::false_type());
 }
 template <int FMT>
 static bool attend_mma_hd(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
@@ -1117,7 +1165,7 @@ static Sched schedule(const KvView &kv, int n_seq) {
   Sched sc{n_seq, kv.Hkv, 0, 0};
   const int64_t pairs = (int64_t)n_seq * kv.Hkv;
   const int64_t cap = (int64_t)kv.table_pages * kv.ps;
-  sc.direct = cap <= 2 * PG_UNIT;
+  sc.direct = cap <= 8 * PG_UNIT;
   sc.N = sc.direct ? (int)pairs : device_sms() * BLOCKS_SM;
   return sc;
 }
