@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
                                              int *__restrict__ n_tiles, PkTile *__restrict__ tiles,
                                              int *__restrict__ off, int *__restrict__ rank,
                                              int *flag) {
-  __shared__ int hist[MAXC + 2];  // sequences of exactly n blocks; then the next free rank
+  __shared__ int hist[MAXC + 2];  // sequences of exactly n blocks; then cnt, then off
+  pk_release();
   __shared__ int warp_tot[32];
   const int C = (n_rows + PK_BLOCK - 1) / PK_BLOCK;
   for (int i = threadIdx.x; i <= C + 1; i += PT) hist[i] = 0;
@@ -121,6 +122,60 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
     for (int b = threadIdx.x & 31; b < n; b += 32)
       tiles[hist[b + 1] + rank[s]] = PkTile{row0, len, b, 0};
   }
+}
+
+// The same plan for few sequences, where the scans' barriers would take longer
+// than counting: off(c) = sum over the sequences of max(0, n - c), and a
+// sequence's rank by comparing it with every other one.
+constexpr int FEW = 256;
+__global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu, int n_seq,
+                                                  int n_rows, int *__restrict__ n_tiles,
+                                                  PkTile *__restrict__ tiles, int *flag) {
+  __shared__ int off[FEW + 1], blocks[FEW], rank[FEW], base[MAXC + 1];
+  __shared__ int warp_tot[FEW / 32];
+  pk_release();
+  const int t = threadIdx.x;
+  const int mine = t <= n_seq ? cu[t] : 0, last = cu[n_seq];  // n_seq may be FEW: one entry more
+  const int next = t < n_seq ? cu[t + 1] : 0;
+  const bool bad = t < n_seq && (mine < 0 || mine > next || next > n_rows);
+  if (t < n_seq) off[t] = mine;
+  if (t == 0) off[n_seq] = last;
+  if (__syncthreads_or(bad)) {  // running maximum of the clamped offsets
+    if (flag && t == 0) atomicOr(flag, PK_BAD_OFFSETS);
+    int v = min(max(t < n_seq ? mine : 0, 0), n_rows);
+    const int lane = t & 31, warp = t >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, x);
+    }
+    if (lane == 31) warp_tot[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; w++) v = max(v, warp_tot[w]);
+    if (t < n_seq) off[t] = v;
+    __syncthreads();
+    if (t == 0) off[n_seq] = max(off[n_seq - 1], min(max(last, 0), n_rows));
+    __syncthreads();
+  }
+  const int n = t < n_seq ? (off[t + 1] - off[t] + PK_BLOCK - 1) / PK_BLOCK : 0;
+  if (t < n_seq) blocks[t] = n;
+  __syncthreads();
+  if (t < n_seq) {
+    int r = 0;
+    for (int s = 0; s < n_seq; s++) r += blocks[s] > n || (blocks[s] == n && s < t);
+    rank[t] = r;
+  }
+  const int C = (n_rows + PK_BLOCK - 1) / PK_BLOCK;
+  for (int c = t; c <= C; c += FEW) {
+    int sum = 0;
+    for (int s = 0; s < n_seq; s++) sum += max(0, blocks[s] - c);
+    base[c] = sum;
+  }
+  __syncthreads();
+  if (t == 0) *n_tiles = base[0];
+  for (int s = t >> 5; s < n_seq; s += FEW / 32)
+    for (int b = t & 31; b < blocks[s]; b += 32)
+      tiles[base[b + 1] + rank[s]] = PkTile{off[s], off[s + 1] - off[s], b, 0};
 }
 
 // --------------------------------------------------------- CUDA-core kernels
@@ -223,8 +278,11 @@ LLM_DEV float half_sum(float v) {
 // Work item of a block: (tile, head, half of the tile's 128 rows).
 LLM_DEV bool item(const int *n_tiles, const PkTile *tiles, int heads, PkTile &t, int &h, int &half) {
   const int i = blockIdx.x >> 1, k = i / heads;
-  if (k >= *n_tiles) return false;
-  t = tiles[k];
+  pk_release();
+  pk_wait();  // the plan, and D for dK/dV, come from the kernels before
+  if (k >= ld_int(n_tiles)) return false;
+  const int4 w = ld_int4(tiles + k);
+  t = PkTile{w.x, w.y, w.z, 0};
   h = i % heads;
   half = blockIdx.x & 1;
   return true;
@@ -434,7 +492,7 @@ __global__ void __launch_bounds__(NT)
         const int64_t li = (int64_t)h * n_rows + t.row0 + q0 + threadIdx.x;
         const bool in = (int)threadIdx.x < nq;
         sL[threadIdx.x] = in ? lse[li] : INFINITY;  // queries past the sequence: P = 0
-        sD[threadIdx.x] = in ? D[li] : 0.f;
+        sD[threadIdx.x] = in ? ld_float(D + li) : 0.f;
       }
       __syncthreads();
       float s[4][4] = {}, dp[4][4] = {};
@@ -489,7 +547,8 @@ constexpr int dkv_smem() { return (4 * HD * TLD + 2 * TB * HD + TB * TB + 2 * TB
 template <typename T, int HD>
 static bool fwd(const PkArgs &a, const PkPlan &p, void *o, float *lse, bool vec) {
   if (!smem_optin((const void *)k_fwd<T, HD>, fwd_smem<HD>())) return false;
-  k_fwd<T, HD><<<(unsigned)(2 * p.cap * a.H), NT, fwd_smem<HD>(), a.s>>>(
+  launch_dependent(
+      k_fwd<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(NT), fwd_smem<HD>(), a.s,
       (const T *)a.qkv, a.ld, p.n_tiles, p.tiles, (T *)o, lse, a.n_rows, a.H, a.Hkv, a.hd, vec);
   count_launch();
   return true;
@@ -500,10 +559,12 @@ static bool bwd(const PkArgs &a, const PkPlan &p, const void *o, const float *ls
   if (!smem_optin((const void *)k_dq<T, HD>, dq_smem<HD>()) ||
       !smem_optin((const void *)k_dkv<T, HD>, dkv_smem<HD>()))
     return false;
-  k_dq<T, HD><<<(unsigned)(2 * p.cap * a.H), NT, dq_smem<HD>(), a.s>>>(
+  launch_dependent(
+      k_dq<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(NT), dq_smem<HD>(), a.s,
       (const T *)a.qkv, a.ld, p.n_tiles, p.tiles, (const T *)o, lse, (const T *)dout, p.D,
       (T *)dqkv, dld, a.n_rows, a.H, a.Hkv, a.hd, vec);
-  k_dkv<T, HD><<<(unsigned)(2 * p.cap * a.Hkv), NT, dkv_smem<HD>(), a.s>>>(
+  launch_dependent(
+      k_dkv<T, HD>, dim3((unsigned)(2 * p.cap * a.Hkv)), dim3(NT), dkv_smem<HD>(), a.s,
       (const T *)a.qkv, a.ld, p.n_tiles, p.tiles, lse, (const T *)dout, p.D, (T *)dqkv, dld,
       a.n_rows, a.H, a.Hkv, a.hd, vec);
   count_launch(2);
@@ -518,6 +579,12 @@ static bool vec4(const PkArgs &a, const void *p) {
 }  // namespace pk
 
 void packed_plan(const PkArgs &a, const PkPlan &p) {
+  if (a.n_seq <= pk::FEW) {
+    pk::k_plan_few<<<1, pk::FEW, 0, a.s>>>(a.cu, a.n_seq, (int)a.n_rows, p.n_tiles, p.tiles,
+                                           a.flag);
+    count_launch();
+    return;
+  }
   pk::k_plan<<<1, pk::PT, 0, a.s>>>(a.cu, a.n_seq, (int)a.n_rows, p.n_tiles, p.tiles, p.off,
                                     p.rank, a.flag);
   count_launch();

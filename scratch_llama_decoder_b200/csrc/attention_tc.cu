@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   static_assert(2 * QSLOTS + 4 * STAGES + 4 + 3 * NQ + 2 <= 48,
                 "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int nqb = (T_all + BQ - 1) / BQ, n_items = PK ? *pk.n_tiles * H : nqb * H * B;
+  const int nqb = (T_all + BQ - 1) / BQ;
   const int G = gridDim.x, cta = blockIdx.x;
   // item -> (query block, head, batch): longest rows (last query blocks) first,
   // in bands of 4 query blocks taken pair by pair (band_item)
@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_sh;
+  if constexpr (PK) pk_wait();  // the plan comes from the kernel before
+  const int n_items = PK ? ld_int(pk.n_tiles) * H : nqb * H * B;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -566,9 +568,9 @@ bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
       !head_map_store(&mo, o, a.hd, a.H, a.n_rows, 1, dw, 8))
     return false;
   const int grid = (int)min(p.cap * a.H, (int64_t)device_sms());
-  k_attn_fwd_tc<true><<<grid, NTHREADS, SMEM_BYTES, a.s>>>(
-      map, mo, lse, 1, 0, a.H, a.Hkv, a.hd, 1.0f / sqrtf((float)a.hd),
-      PkView{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)o, dw}, flag);
+  launch_dependent(k_attn_fwd_tc<true>, dim3(grid), dim3(NTHREADS), SMEM_BYTES, a.s, map, mo, lse, 1,
+                   0, a.H, a.Hkv, a.hd, 1.0f / sqrtf((float)a.hd),
+                   PkView{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)o, dw}, flag);
   count_launch();
   return true;
 }

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  qred = qsync + 32;       // [4]: per lane quarter, its rows' D parts written
   static_assert(6 + 4 * STAGES + 18 <= 48, "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int nqb = (T_all + BQ - 1) / BQ, n_items = PK ? *pk.n_tiles * H : nqb * H * B;
+  const int nqb = (T_all + BQ - 1) / BQ;
   const int G = gridDim.x, cta = blockIdx.x;
   // item -> (query block, head, batch): longest rows (last query blocks) first,
   // in bands of 4 query blocks taken pair by pair (band_item)
@@ -227,6 +227,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_sh;
+  if constexpr (PK) {
+    pk_release();
+    pk_wait();  // the plan comes from the kernel before
+  }
+  const int n_items = PK ? ld_int(pk.n_tiles) * H : nqb * H * B;
 
   if (warp == 0) {
     // ---------------------------------------------- TMA producer (warp)
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  qsync = drain + 16;   // [4]: per lane quarter, its rows of dK, dV staged
   static_assert(4 + 3 * STAGES + 10 <= 48, "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int nkb_all = (T_all + BK - 1) / BK, n_items = PK ? *pk.n_tiles * Hkv : nkb_all * Hkv * B;
+  const int nkb_all = (T_all + BK - 1) / BK;
   const int G = gridDim.x, cta = blockIdx.x;
   const int grp = H / Hkv;
   // item -> (key block, kv head, batch), first key blocks first in bands of 4
@@ -651,6 +656,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_sh;
+  if constexpr (PK) pk_wait();  // the plan, and D, come from the kernels before
+  const int n_items = PK ? ld_int(pk.n_tiles) * Hkv : nkb_all * Hkv * B;
 
   if (warp == 0) {
     // ---------------------------------------------- TMA producer (warp)
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             sD[s * 128 + i] = 0.f;
           } else if (!bulk_l) {
             sL[s * 128 + i] = lse[base + i];
-            sD[s * 128 + i] = Dv[base + i];
+            sD[s * 128 + i] = PK ? ld_float(Dv + base + i) : Dv[base + i];
           }
         }
         mbar_arrive(ld_full + 8 * s);
@@ -1045,12 +1052,12 @@ bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float 
   const float scale = 1.0f / sqrtf((float)a.hd);
   const PkView pk{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)dqkv, dld};
   // L and D rows start anywhere: read by the lanes
-  k_attn_dq_tc<true><<<(int)min(p.cap * a.H, sms), NTHREADS, DQ_SMEM, a.s>>>(
-      mq, md, mo, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H, a.Hkv, a.hd,
-      scale, 0, pk, flag);
-  k_attn_dkv_tc<true><<<(int)min(p.cap * a.Hkv, sms), NTHREADS, KV_SMEM, a.s>>>(
-      mq, md, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H, a.Hkv, a.hd,
-      scale, 0, pk, flag);
+  launch_dependent(k_attn_dq_tc<true>, dim3((int)min(p.cap * a.H, sms)), dim3(NTHREADS), DQ_SMEM, a.s,
+                   mq, md, mo, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H,
+                   a.Hkv, a.hd, scale, 0, pk, flag);
+  launch_dependent(k_attn_dkv_tc<true>, dim3((int)min(p.cap * a.Hkv, sms)), dim3(NTHREADS), KV_SMEM,
+                   a.s, mq, md, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H,
+                   a.Hkv, a.hd, scale, 0, pk, flag);
   count_launch(2);
   return true;
 }

@@ -37,7 +37,7 @@ struct Item {
   int blk, h, b, row0, T;
 };
 LLM_DEV Item pk_item(const PkView &pk, int item, int heads, bool keys) {
-  const int4 t = *reinterpret_cast<const int4 *>(pk.tiles + item / heads);
+  const int4 t = ld_int4(pk.tiles + item / heads);
   const int n = (t.y + PK_BLOCK - 1) / PK_BLOCK;
   return Item{keys ? n - 1 - t.z : t.z, item % heads, 0, t.x, t.y};
 }

@@ -16,6 +16,31 @@ template <typename T> LLM_DEV T from_f(float x);
 template <> LLM_DEV float from_f<float>(float x) { return x; }
 template <> LLM_DEV __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// Programmatic dependent launch of the kernels that follow one another inside
+// a call: pk_release lets the next one's blocks start once every block of this
+// one has passed it; pk_wait blocks until the kernels before are complete and
+// their writes visible.
+LLM_DEV void pk_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+LLM_DEV void pk_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads of what those kernels wrote: volatile, so that they stay behind the
+// wait (a load through a const restrict pointer may be moved before it).
+LLM_DEV int ld_int(const int *p) {
+  int v;
+  asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+LLM_DEV int4 ld_int4(const void *p) {
+  int4 v;
+  asm volatile("ld.global.cg.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+LLM_DEV float ld_float(const float *p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- reductions
 // sigmoid by the fast exponential and reciprocal intrinsics (relative error
 // ~1e-6, far below the bf16 rounding of the results)

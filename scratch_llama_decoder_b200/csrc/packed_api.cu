@@ -56,7 +56,7 @@ bool kv_view(const llm_kv *kv, KvView *v) {
   return true;
 }
 bool paged_ok(const KvView &v, int n_seq, int H) {
-  const int64_t units = ((int64_t)v.table_pages * v.ps + PG_UNIT - 1) / PG_UNIT;
+  const int64_t units = ((int64_t)v.table_pages * v.ps + PG_UNIT - 1) / PG_UNIT + PG_SETUP;
   return n_seq >= 0 && n_seq <= PG_MAX_SEQ && heads_ok(H, v.Hkv, v.hd) &&
          units * n_seq < ((int64_t)1 << 31);
 }

@@ -274,15 +274,18 @@ __global__ void __launch_bounds__(RW_THREADS)
 
 // --------------------------------------------------------------- attention
 // The work of a call is the (sequence, kv head) pairs in order, each
-// ceil(len / 64) units of 64 positions: W units in a row, of which block i of
-// N (at most W, so that none is empty) takes [W i / N, W (i + 1) / N) whatever
-// the lengths are.  A pair that lies
+// ceil(len / 64) units of 64 positions behind PG_SETUP units that stand for what a
+// pair costs before its first position (its queries, the first loads' latency,
+// the warps' joining: about that of 3 units; without them the blocks that got
+// many short sequences ran 1.4 times as long as the others): W units in a row,
+// of which block i of N (at most W, so that none is empty) takes
+// [W i / N, W (i + 1) / N) whatever the lengths are.  A pair that lies
 // in one block is finished there; a pair cut between blocks leaves, per block,
 // the running maximum, sum and weighted values of its part in the workspace,
 // and a second kernel joins the parts in order.  A block's range cuts at most
 // its first and its last pair: two slots per block.
 constexpr int AT = 128;       // threads
-constexpr int BLOCKS_SM = 4;  // blocks per SM that the split counts on
+constexpr int BLOCKS_SM = 4;  // most blocks per SM that the split counts on
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct Sched {
@@ -295,6 +298,9 @@ LLM_DEV int clamped_len(const KvView &kv, const int32_t *lens, int s) {
   if (bad && kv.flag) atomicOr(kv.flag, PK_BAD_PAGE);
   return bad ? (n < 0 ? 0 : (int)cap) : n;
 }
+LLM_DEV int units_of(int len) {
+  return len > 0 ? PG_SETUP + (len + PG_UNIT - 1) / PG_UNIT : 0;
+}
 // pre[s] = units of the sequences before s, per kv head (n_seq + 1 entries).
 LLM_DEV void unit_prefix(const KvView &kv, const int32_t *lens, int n_seq, int *pre) {
   __shared__ int tot[AT / 32];
@@ -302,7 +308,7 @@ LLM_DEV void unit_prefix(const KvView &kv, const int32_t *lens, int n_seq, int *
   int carry = 0;
   for (int s0 = 0; s0 < n_seq; s0 += AT) {
     const int s = s0 + threadIdx.x;
-    int v = s < n_seq ? (clamped_len(kv, lens, s) + PG_UNIT - 1) / PG_UNIT : 0;
+    int v = s < n_seq ? units_of(clamped_len(kv, lens, s)) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, v, o);
@@ -343,24 +349,30 @@ __global__ void __launch_bounds__(AT)
   constexpr int EPL = HD / 8, NC = (EPL + 7) / 8;  // columns a lane, 8-element pieces
   extern __shared__ int pre[];
   __shared__ float sm[AT / 32][GT][HD + 2];
-  unit_prefix(kv, lens, sc.n_seq, pre);
-  if (!sc.direct && blockIdx.x == 0)
-    for (int s = threadIdx.x; s <= sc.n_seq; s += AT) pre_out[s] = pre[s];
+  pk_release();
+  if (!sc.direct) {
+    unit_prefix(kv, lens, sc.n_seq, pre);
+    if (blockIdx.x == 0)
+      for (int s = threadIdx.x; s <= sc.n_seq; s += AT) pre_out[s] = pre[s];
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7, ks = lane >> 3;
   const int grp = H / kv.Hkv, hd = kv.hd;
   const float sl2 = LOG2E / sqrtf((float)hd);
-  const int64_t W = (int64_t)pre[sc.n_seq] * kv.Hkv;
-  const int N = (int)min((int64_t)sc.N, W);
-  if (!sc.direct && (int)blockIdx.x >= N) return;
-  int64_t w = sc.direct ? 0 : block_begin(W, blockIdx.x, N);
-  const int64_t end = sc.direct ? 1 : block_begin(W, blockIdx.x + 1, N);
+  int64_t w = 0, end = 1;
+  if (!sc.direct) {
+    const int64_t W = (int64_t)pre[sc.n_seq] * kv.Hkv;
+    const int N = (int)min((int64_t)sc.N, W);
+    if ((int)blockIdx.x >= N) return;
+    w = block_begin(W, blockIdx.x, N);
+    end = block_begin(W, blockIdx.x + 1, N);
+  }
   for (int piece = 0; w < end; piece++) {
     int s, g, u0, nu, units;
     if (sc.direct) {
       s = blockIdx.x / kv.Hkv;
       g = blockIdx.x % kv.Hkv;
-      u0 = 0;
-      nu = units = pre[s + 1] - pre[s];
+      u0 = nu = units = 0;
+      if (threadIdx.x == 0) clamped_len(kv, lens, s);  // a bad length is flagged
       w = end;
     } else {
       s = seq_at(pre, sc.n_seq, w, kv.Hkv);
@@ -372,7 +384,8 @@ __global__ void __launch_bounds__(AT)
       w += nu;
     }
     const int len = min(max(lens[s], 0), (int)min((int64_t)kv.table_pages * kv.ps, (int64_t)INT_MAX));
-    const int j0 = u0 * PG_UNIT, j1 = min(len, (u0 + nu) * PG_UNIT);
+    const int j0 = sc.direct ? 0 : max(u0 - PG_SETUP, 0) * PG_UNIT;
+    const int j1 = sc.direct ? len : min(len, max(u0 + nu - PG_SETUP, 0) * PG_UNIT);
     for (int r0 = 0; r0 < grp; r0 += GT) {
       float qv[GT][EPL], acc[GT][EPL], m[GT], l[GT];
 #pragma unroll
@@ -521,6 +534,9 @@ __global__ void __launch_bounds__(AT)
 // The bfloat16 and float16 rounding of the weights (2^-9 and 2^-12) is the
 // only rounding below 32 bits; the sum l takes them unrounded.
 constexpr int NW = AT / 32;
+// Blocks per SM: what the registers of a lane's operands leave room for.
+constexpr int mma_blocks(int HD, int NT) { return NT == 2 ? 2 : HD == 128 ? 3 : 4; }
+static_assert(mma_blocks(32, 1) <= BLOCKS_SM, "the workspace counts BLOCKS_SM");
 // log2 units a maximum may grow before O is rescaled, and the log2 of a weight
 // at its reference: a float16 weight is at most 2^(14 + 1), and those below
 // 2^-14 keep steps of 2^-24, 2^-38 of the reference
@@ -607,9 +623,8 @@ LLM_DEV void half_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
 template <int HD, int HEADS>
 LLM_DEV void finish(const float *sm, int grp, int r0, int hd, bool whole, __nv_bfloat16 *o,
                     float *lse, float *rec) {
-  for (int i = threadIdx.x; i < HEADS * HD; i += AT) {
+  for (int i = threadIdx.x; i < min(HEADS, grp - r0) * HD; i += AT) {
     const int r = i / HD, e = i % HD;
-    if (r0 + r >= grp) continue;
     float M = -INFINITY;
 #pragma unroll
     for (int x = 0; x < NW; x++) M = fmaxf(M, sm[(x * HEADS + r) * (HD + 2) + HD]);
@@ -636,7 +651,7 @@ LLM_DEV void finish(const float *sm, int grp, int r0, int hd, bool whole, __nv_b
 }
 
 template <int FMT, int HD, int NT, int SB, int GC, bool BIG>
-__global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
+__global__ void __launch_bounds__(AT, mma_blocks(HD, NT))
     k_attend_mma(const KvView kv, const __nv_bfloat16 *__restrict__ q, int64_t q_ld,
                  const int32_t *__restrict__ lens, const Sched sc, int H,
                  __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
@@ -653,6 +668,7 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
   const float sl2 = LOG2E / sqrtf((float)HD);
   int64_t w = 0, end = 1;
   if (!sc.direct) {
+    pk_release();
     unit_prefix(kv, lens, sc.n_seq, pre);
     if (blockIdx.x == 0)
       for (int s = threadIdx.x; s <= sc.n_seq; s += AT) pre_out[s] = pre[s];
@@ -681,12 +697,12 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
       w += nu;
       whole = nu == units;
       const int64_t cap = (int64_t)kv.table_pages * kv.ps;
-      j0 = u0 * PG_UNIT;
-      j1 = (int)min(min((int64_t)lens[s], cap), (int64_t)(u0 + nu) * PG_UNIT);
+      j0 = max(u0 - PG_SETUP, 0) * PG_UNIT;
+      j1 = (int)min(min((int64_t)lens[s], cap), (int64_t)max(u0 + nu - PG_SETUP, 0) * PG_UNIT);
     }
     const int32_t *table = kv.table + (int64_t)s * kv.table_ld;
     const int64_t vrows = (int64_t)kv.Hkv * kv.ps;  // from a key's row to its value's
-    const int nit = (j1 - j0 + NW * KB - 1) / (NW * KB);
+    const int nit = (max(j1 - j0, 0) + NW * KB - 1) / (NW * KB);
     for (int r0 = 0; r0 < grp; r0 += HEADS) {
       // q^T fragments: head lg of each tile, columns as K's words hold them
       uint32_t qf[NT][HD / 16][2];
@@ -1024,21 +1040,23 @@ __global__ void __launch_bounds__(AT, NT == 2 ? 2 : HD == 128 ? 3 : 4)
   }
 }
 
-// Joins the parts of every cut pair, in order; a sequence of length 0 gets
-// o = 0 and L = -inf.
+// Joins the parts of every cut pair, in order, AT outputs a block; a sequence
+// of length 0 gets o = 0 and L = -inf.
 template <typename T>
 __global__ void __launch_bounds__(AT)
     k_join(const int *__restrict__ pre, const float *__restrict__ part, const Sched sc, int H,
            int hd, T *__restrict__ o, float *__restrict__ lse) {
   const int s = blockIdx.x / sc.Hkv, g = blockIdx.x % sc.Hkv, grp = H / sc.Hkv;
-  const int units = pre[s + 1] - pre[s];
-  const int64_t W = (int64_t)pre[sc.n_seq] * sc.Hkv;
-  const int64_t w0 = (int64_t)pre[s] * sc.Hkv + (int64_t)g * units;
+  const int i = blockIdx.y * AT + threadIdx.x;
+  pk_wait();  // the parts and the prefix come from the kernel before
+  if (i >= grp * hd) return;
+  const int r = i / hd, e = i % hd;
+  const int before = ld_int(pre + s), units = ld_int(pre + s + 1) - before;
+  const int64_t W = (int64_t)ld_int(pre + sc.n_seq) * sc.Hkv;
+  const int64_t w0 = (int64_t)before * sc.Hkv + (int64_t)g * units;
   if (units == 0) {
-    for (int i = threadIdx.x; i < grp * hd; i += AT)
-      o[((int64_t)s * H + g * grp) * hd + i] = from_f<T>(0.f);
-    if (lse)
-      for (int i = threadIdx.x; i < grp; i += AT) lse[(int64_t)s * H + g * grp + i] = -INFINITY;
+    o[((int64_t)s * H + g * grp) * hd + i] = from_f<T>(0.f);
+    if (e == 0 && lse) lse[(int64_t)s * H + g * grp + r] = -INFINITY;
     return;
   }
   const int N = (int)min((int64_t)sc.N, W);
@@ -1049,40 +1067,44 @@ __global__ void __launch_bounds__(AT)
   const int first = block_begin(W, b0, N) < w0 ? 1 : 0;
   const int64_t step = (int64_t)grp * (hd + 2);
   constexpr int U = 8;  // parts whose loads are in flight together
-  for (int i = threadIdx.x; i < grp * hd; i += AT) {
-    const int r = i / hd, e = i % hd;
-    float M = -INFINITY, L = 0.f, v = 0.f;
-    for (int b = b0; b <= b1; b += U) {
-      float pm[U], pl[U], pv[U], mn = M;
+  float M = -INFINITY, L = 0.f, v = 0.f;
+  for (int b = b0; b <= b1; b += U) {
+    float pm[U], pl[U], pv[U], mn = M;
 #pragma unroll
-      for (int k = 0; k < U; k++) {
-        const bool in = b + k <= b1;
-        const float *rec = part + (2 * (in ? b + k : b0) + (b + k == b0 || !in ? first : 0)) * step +
-                           r * (hd + 2);
-        pm[k] = in ? __ldcg(rec) : -INFINITY;
-        pl[k] = __ldcg(rec + 1);
-        pv[k] = __ldcg(rec + 2 + e);
-      }
-#pragma unroll
-      for (int k = 0; k < U; k++) mn = fmaxf(mn, pm[k]);
-      const float ref = mn == -INFINITY ? 0.f : mn, a = exp2f(M - ref);
-      L *= a;
-      v *= a;
-#pragma unroll
-      for (int k = 0; k < U; k++) {
-        const float f = exp2f(pm[k] - ref);
-        if (b + k <= b1) {
-          L = fmaf(f, pl[k], L);
-          v = fmaf(f, pv[k], v);
-        }
-      }
-      M = mn;
+    for (int k = 0; k < U; k++) {
+      const bool in = b + k <= b1;
+      const float *rec = part + (2 * (in ? b + k : b0) + (b + k == b0 || !in ? first : 0)) * step +
+                         r * (hd + 2);
+      pm[k] = in ? ld_float(rec) : -INFINITY;
+      pl[k] = ld_float(rec + 1);
+      pv[k] = ld_float(rec + 2 + e);
     }
-    o[((int64_t)s * H + g * grp) * hd + i] = from_f<T>(L == 0.f ? 0.f : v / L);
-    if (e == 0 && lse) lse[(int64_t)s * H + g * grp + r] = (M + log2f(L)) * LN2;
+#pragma unroll
+    for (int k = 0; k < U; k++) mn = fmaxf(mn, pm[k]);
+    const float ref = mn == -INFINITY ? 0.f : mn, a = exp2f(M - ref);
+    L *= a;
+    v *= a;
+#pragma unroll
+    for (int k = 0; k < U; k++) {
+      const float f = exp2f(pm[k] - ref);
+      if (b + k <= b1) {
+        L = fmaf(f, pl[k], L);
+        v = fmaf(f, pv[k], v);
+      }
+    }
+    M = mn;
   }
+  o[((int64_t)s * H + g * grp) * hd + i] = from_f<T>(L == 0.f ? 0.f : v / L);
+  if (e == 0 && lse) lse[(int64_t)s * H + g * grp + r] = (M + log2f(L)) * LN2;
 }
 
+template <typename T>
+static void join(const PagedArgs &a, const Sched &sc, const int *pre, const float *part) {
+  launch_dependent(k_join<T>,
+                   dim3((unsigned)(a.n_seq * a.kv.Hkv), cdiv((int64_t)a.H / a.kv.Hkv * a.kv.hd, AT)),
+                   dim3(AT), 0, a.s, pre, part, sc, a.H, a.kv.hd, (T *)a.o, a.lse);
+  count_launch();
+}
 template <typename T, int FMT, int HD>
 static bool attend(const PagedArgs &a, const Sched &sc, int *pre, float *part, bool vec) {
   const int grp = a.H / a.kv.Hkv, smem = 4 * (a.n_seq + 1);
@@ -1095,22 +1117,21 @@ static bool attend(const PagedArgs &a, const Sched &sc, int *pre, float *part, b
   };
   if (!(grp == 1 ? go(k_attend<T, FMT, HD, 1>) : go(k_attend<T, FMT, HD, 4>))) return false;
   if (!sc.direct) {
-    k_join<T><<<a.n_seq * a.kv.Hkv, AT, 0, a.s>>>(pre, part, sc, a.H, a.kv.hd, (T *)a.o, a.lse);
-    count_launch();
+    join<T>(a, sc, pre, part);
   }
   return true;
 }
 template <int FMT, int HD, int NT, int SB, int GC, bool BIG>
-static bool attend_mma(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
+static bool attend_mma(const PagedArgs &a, Sched sc, int *pre, float *part) {
   using T = __nv_bfloat16;
   auto kern = k_attend_mma<FMT, HD, NT, SB, GC, BIG>;
   if (!smem_optin((const void *)kern, 4 * (PG_MAX_SEQ + 1))) return false;
+  if (!sc.direct) sc.N = device_sms() * mma_blocks(HD, NT);
   kern<<<sc.N, AT, sc.direct ? 0 : 4 * (a.n_seq + 1), a.s>>>(
       a.kv, (const T *)a.q, a.q_ld, a.lens, sc, a.H, (T *)a.o, a.lse, pre, part);
   count_launch();
   if (!sc.direct) {
-    k_join<T><<<a.n_seq * a.kv.Hkv, AT, 0, a.s>>>(pre, part, sc, a.H, a.kv.hd, (T *)a.o, a.lse);
-    count_launch();
+    join<T>(a, sc, pre, part);
   }
   return true;
 }
@@ -1127,11 +1148,10 @@ static bool attend_mma_nt(const PagedArgs &a, const Sched &sc, int *pre, float *
 }
 template <int FMT>
 static bool attend_mma_hd(const PagedArgs &a, const Sched &sc, int *pre, float *part) {
-  constexpr int SB = 2;
   switch (a.kv.hd) {
-    case 32: return attend_mma_nt<FMT, 32, SB>(a, sc, pre, part);
-    case 64: return attend_mma_nt<FMT, 64, SB>(a, sc, pre, part);
-    default: return attend_mma_nt<FMT, 128, FMT == KV_BF16 ? 1 : SB>(a, sc, pre, part);
+    case 32: return attend_mma_nt<FMT, 32, 4>(a, sc, pre, part);
+    case 64: return attend_mma_nt<FMT, 64, 2>(a, sc, pre, part);
+    default: return attend_mma_nt<FMT, 128, FMT == KV_BF16 ? 1 : 2>(a, sc, pre, part);
   }
 }
 // The tensor-core kernels: bfloat16 queries over a bfloat16 or 8-bit cache,

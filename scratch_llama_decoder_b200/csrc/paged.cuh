@@ -39,6 +39,7 @@ void kv_read(const KvView &kv, const int32_t *cu, const int32_t *start, int n_se
 // Attention of one query per sequence over its first lens[s] positions.
 constexpr int PG_MAX_SEQ = 8192;  // sequences of one call
 constexpr int PG_UNIT = 64;       // positions of a unit of work
+constexpr int PG_SETUP = 3;       // units that stand for what a (sequence, kv head) costs besides
 struct PagedArgs {
   KvView kv;
   const void *q;
