@@ -55,11 +55,11 @@ LLM_DEV int block_scan(int v, int *warp_tot) {
 __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int n_seq, int n_rows,
                                              int *__restrict__ n_tiles, PkTile *__restrict__ tiles,
                                              int *__restrict__ off, int *__restrict__ rank,
-                                             int *flag) {
+                                             int block, int *flag) {
   __shared__ int hist[MAXC + 2];  // sequences of exactly n blocks; then cnt, then off
   pk_release();
   __shared__ int warp_tot[32];
-  const int C = (n_rows + PK_BLOCK - 1) / PK_BLOCK;
+  const int C = (n_rows + block - 1) / block;
   for (int i = threadIdx.x; i <= C + 1; i += PT) hist[i] = 0;
   // offsets: running maximum of the clamped entries
   int carry = 0;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
   if (bad && flag) atomicOr(flag, PK_BAD_OFFSETS);
   __syncthreads();
   for (int s = threadIdx.x; s < n_seq; s += PT) {
-    const int n = (off[s + 1] - off[s] + PK_BLOCK - 1) / PK_BLOCK;
+    const int n = (off[s + 1] - off[s] + block - 1) / block;
     // the rank among sequences of as many blocks, completed below
     rank[s] = n ? atomicAdd(&hist[n], 1) : 0;
   }
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
   if (threadIdx.x == 0) hist[C + 1] = 0;
   __syncthreads();
   for (int s = threadIdx.x; s < n_seq; s += PT) {
-    const int n = (off[s + 1] - off[s] + PK_BLOCK - 1) / PK_BLOCK;
+    const int n = (off[s + 1] - off[s] + block - 1) / block;
     if (n) rank[s] += hist[n + 1];  // after every longer sequence
   }
   __syncthreads();
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
   if (threadIdx.x == 0) *n_tiles = carry;
   __syncthreads();
   for (int s = threadIdx.x >> 5; s < n_seq; s += PT / 32) {
-    const int row0 = off[s], len = off[s + 1] - row0, n = (len + PK_BLOCK - 1) / PK_BLOCK;
+    const int row0 = off[s], len = off[s + 1] - row0, n = (len + block - 1) / block;
     for (int b = threadIdx.x & 31; b < n; b += 32)
       tiles[hist[b + 1] + rank[s]] = PkTile{row0, len, b, 0};
   }
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
 constexpr int FEW = 256;
 __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu, int n_seq,
                                                   int n_rows, int *__restrict__ n_tiles,
-                                                  PkTile *__restrict__ tiles, int *flag) {
+                                                  PkTile *__restrict__ tiles, int block, int *flag) {
   __shared__ int off[FEW + 1], blocks[FEW], rank[FEW], base[MAXC + 1];
   __shared__ int warp_tot[FEW / 32];
   pk_release();
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
     if (t == 0) off[n_seq] = max(off[n_seq - 1], min(max(last, 0), n_rows));
     __syncthreads();
   }
-  const int n = t < n_seq ? (off[t + 1] - off[t] + PK_BLOCK - 1) / PK_BLOCK : 0;
+  const int n = t < n_seq ? (off[t + 1] - off[t] + block - 1) / block : 0;
   if (t < n_seq) blocks[t] = n;
   __syncthreads();
   if (t < n_seq) {
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
     for (int s = 0; s < n_seq; s++) r += blocks[s] > n || (blocks[s] == n && s < t);
     rank[t] = r;
   }
-  const int C = (n_rows + PK_BLOCK - 1) / PK_BLOCK;
+  const int C = (n_rows + block - 1) / block;
   for (int c = t; c <= C; c += FEW) {
     int sum = 0;
     for (int s = 0; s < n_seq; s++) sum += max(0, blocks[s] - c);
@@ -578,20 +578,21 @@ static bool vec4(const PkArgs &a, const void *p) {
 
 }  // namespace pk
 
-void packed_plan(const PkArgs &a, const PkPlan &p) {
+void packed_plan(const PkArgs &a, const PkPlan &p, int block) {
   if (a.n_seq <= pk::FEW) {
     pk::k_plan_few<<<1, pk::FEW, 0, a.s>>>(a.cu, a.n_seq, (int)a.n_rows, p.n_tiles, p.tiles,
-                                           a.flag);
+                                           block, a.flag);
     count_launch();
     return;
   }
   pk::k_plan<<<1, pk::PT, 0, a.s>>>(a.cu, a.n_seq, (int)a.n_rows, p.n_tiles, p.tiles, p.off,
-                                    p.rank, a.flag);
+                                    p.rank, block, a.flag);
   count_launch();
 }
 
 bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse) {
   using namespace pk;
+  packed_plan(a, p, PK_BLOCK);
   const bool v = vec4(a, a.qkv);
   if (a.dt == DT_BF16) {
     using T = __nv_bfloat16;
@@ -606,6 +607,7 @@ bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse) {
 bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                      const void *dout, void *dqkv, int64_t dld) {
   using namespace pk;
+  packed_plan(a, p, PK_BLOCK);
   const bool v = vec4(a, a.qkv) && vec4(a, dout);
   if (a.dt == DT_BF16) {
     using T = __nv_bfloat16;

@@ -1,0 +1,505 @@
+// tcgen05 flash attention over packed sequences, forward, head sizes 32, 64
+// and 128 (bf16 operands, fp32 softmax and accumulators).
+//
+// One CTA works on two 128-query tiles at once, streams A and B, that share
+// their key and value tiles: two query heads of one kv head at the same rows
+// where a kv head has an even number of them (HEADS), else two consecutive
+// row blocks of one head (a stream may then have one key block less, or no
+// rows).  Per stream and key block of 128:
+//   S = Q K_j^T         (M 128, N 128; operands K-major in shared memory)
+//   P = 2^(S c - m)     softmax: 4 warps, a thread holds one row whole
+//   O += P V_j          (M 128, N head size; A = P from TMEM, V MN-major)
+// While one stream's thread quadruple waits for its products, the other's
+// computes: the exponentials (the SFU gives 16 a clock and SM, a 128 x 128
+// block has 16384) bound the kernel, and one stream alone left the SFU idle
+// half the time (the one-tile kernel of the rectangular batch: 1900 cycles a
+// block).  A row per thread needs no exchange between threads: the running
+// maximum moves only when a block exceeds it by 2^8 (then the thread rescales
+// its own row of O in TMEM), and NP of every 16 pairs of exponentials run as a
+// polynomial on the FMA pipe (exp2_poly2).
+// TMEM: S_A, S_B (128 columns each), O_A, O_B (head size each).  Heads to 64
+// leave room for P beside S (SEP), so S_{j+1} is computed while block j's
+// softmax runs; at head 128 P takes the first half of S's columns, and S_{j+1}
+// follows O += P V_j.
+// Warps: 0 TMA producer; 1, 2 MMA issuers of A and B (warp 1 also TMEM);
+// 4-7 and 8-11 softmax of A and B.  Every wait is bounded (FLAG_TIMEOUT).
+// Rows of a tile past its sequence's end are another's: masked as keys, zeroed
+// in V before they meet a zero weight, not stored.
+#include "attn_tma.cuh"
+#include "common.cuh"
+#include "tcgen05.cuh"
+
+namespace llm {
+namespace attn_pk_tc {
+
+using namespace tc;
+using namespace attn_maps;
+
+constexpr int SUB_BYTES = 128 * 64 * 2;  // 128 rows x 64 bf16, 128-byte swizzle
+constexpr int NTHREADS = 384;
+constexpr int TMEM_COLS = 512;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LAZY = 8.f;  // log2 units a row maximum may grow before O is rescaled
+constexpr int NP = 4;        // polynomial pairs of every 16
+constexpr int BAR_BYTES = 512;
+
+template <int HD>
+struct Cfg {
+  static constexpr int SUB = HD / 64, TILE = SUB * SUB_BYTES;
+  static constexpr bool SEP = HD == 64;
+  static constexpr int QS = HD == 64 ? 2 : 1;   // Q slots of a stream
+  static constexpr int KST = HD == 64 ? 3 : 2;  // K and V ring stages
+  static constexpr int SMEM = (2 * QS + 2 * KST) * TILE + BAR_BYTES + 1024;
+  // TMEM columns
+  static constexpr int S(int x) { return 128 * x; }
+  static constexpr int O(int x) { return 256 + HD * x; }
+  static constexpr int P(int x) { return SEP ? 384 + 64 * x : 128 * x; }
+};
+
+// An item: what the streams do.
+struct Work {
+  int row0, T, g;    // sequence, kv head
+  int q[2], h[2];    // row block (of 128) and head of each stream
+  int n[2], nj;      // key blocks of each stream (0: no rows), of the item
+};
+template <bool HEADS>
+LLM_DEV Work work(const PkView &pk, int item, int H, int Hkv) {
+  const int heads = HEADS ? H / 2 : H, grp = H / Hkv;
+  const int4 t = ld_int4(pk.tiles + item / heads);
+  const int i = item % heads;
+  Work w;
+  w.row0 = t.x;
+  w.T = t.y;
+  if (HEADS) {
+    w.h[0] = 2 * i;
+    w.h[1] = 2 * i + 1;
+    w.q[0] = w.q[1] = t.z;
+    w.n[0] = w.n[1] = t.z + 1;
+  } else {
+    w.h[0] = w.h[1] = i;
+    w.q[0] = 2 * t.z;
+    w.q[1] = 2 * t.z + 1;
+    w.n[0] = 2 * t.z + 1;
+    w.n[1] = w.q[1] * 128 < t.y ? 2 * t.z + 2 : 0;
+  }
+  w.g = w.h[0] / grp;
+  w.nj = max(w.n[0], w.n[1]);
+  return w;
+}
+
+template <int NPAIRS>
+LLM_DEV float2 exp2_some(float2 x, int i) {
+  return ((i & 15) * NPAIRS) % 16 < NPAIRS ? exp2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
+}
+// 32 scores to weights 2^(s sl2 - mr), packed; their sum is added to acc.
+template <bool POLY>
+LLM_DEV void weights(const float *sv, float sl2, float mr, uint32_t *w, float2 &acc) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 x = __ffma2_rn(make_float2(sv[i], sv[i + 1]), make_float2(sl2, sl2),
+                                make_float2(-mr, -mr));
+    const float2 p = POLY ? exp2_some<NP>(x, i / 2) : make_float2(ex2(x.x), ex2(x.y));
+    acc = __fadd2_rn(acc, p);
+    w[i / 2] = pack_bf16(p.x, p.y);
+  }
+}
+LLM_DEV void tmem_st32u(uint32_t taddr, const uint32_t *w) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+      "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]),
+      "r"(w[15]), "r"(w[16]), "r"(w[17]), "r"(w[18]), "r"(w[19]), "r"(w[20]), "r"(w[21]),
+      "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]), "r"(w[28]),
+      "r"(w[29]), "r"(w[30]), "r"(w[31])
+      : "memory");
+}
+
+template <int HD, bool HEADS>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    k_attn_fwd_pair(const __grid_constant__ CUtensorMap tm_qkv,
+                    const __grid_constant__ CUtensorMap tm_o, float *__restrict__ lse, int H,
+                    int Hkv, int hd, float scale, const PkView pk, int *gflag) {
+  using C = Cfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *sQ = smem, *sK = sQ + 2 * C::QS * C::TILE, *sV = sK + C::KST * C::TILE;
+  uint64_t *bars = (uint64_t *)(sV + C::KST * C::TILE);
+  uint32_t *tmem_sh = (uint32_t *)(bars + 48);
+  volatile int *abort_sh = (volatile int *)(tmem_sh + 1);
+  const uint32_t b0 = smem_u32(bars);
+  const uint32_t q_full = b0, q_empty = q_full + 16 * C::QS,  // [stream][slot]
+                 k_full = q_empty + 16 * C::QS, k_empty = k_full + 8 * C::KST,
+                 v_full = k_empty + 8 * C::KST, v_empty = v_full + 8 * C::KST,
+                 s_full = v_empty + 8 * C::KST, s_free = s_full + 16, p_full = s_free + 16,
+                 o_done = p_full + 16, drain = o_done + 16;  // [stream] each
+  static_assert(4 * C::QS + 4 * C::KST + 10 <= 48, "barriers overlap the TMEM address word");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int G = gridDim.x, cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    *abort_sh = 0;
+    for (int i = 0; i < 2 * C::QS; i++) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1 + 4);  // the last S product; each warp's part of O stored
+    }
+    for (int s = 0; s < C::KST; s++) {
+      mbar_init(k_full + 8 * s, 1);
+      mbar_init(k_empty + 8 * s, 2);  // both streams
+      mbar_init(v_full + 8 * s, 1);
+      mbar_init(v_empty + 8 * s, 2);
+    }
+    for (int x = 0; x < 2; x++) {
+      mbar_init(s_full + 8 * x, 1);
+      mbar_init(s_free + 8 * x, 4);
+      mbar_init(p_full + 8 * x, 4);
+      mbar_init(o_done + 8 * x, 1);
+      mbar_init(drain + 8 * x, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_sh)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_sh;
+  pk_wait();  // the plan comes from the kernel before
+  const int n_items = ld_int(pk.n_tiles) * (HEADS ? H / 2 : H);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------ TMA producer
+      int gb = 0, nq[2] = {0, 0};  // key blocks, Q tiles of each stream issued
+      bool ok = true;
+      for (int r = 0; ok; r++) {
+        const int item = sched_item(r, G, cta);
+        if (item >= n_items) break;
+        const Work w = work<HEADS>(pk, item, H, Hkv);
+        for (int x = 0; x < 2 && ok; x++) {
+          if (w.n[x] == 0) continue;
+          const int sl = nq[x] % C::QS;
+          const uint32_t bar = 8 * (x * C::QS + sl);
+          ok = mbar_wait(q_empty + bar, ((nq[x] / C::QS) & 1) ^ 1, abort_sh, gflag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(q_full + bar, C::TILE);
+          for (int c = 0; c < C::SUB; c++)
+            tma_load_3d(smem_u32(sQ + (x * C::QS + sl) * C::TILE + c * SUB_BYTES), &tm_qkv, 64 * c,
+                        w.h[x], w.row0 + w.q[x] * 128, q_full + bar);
+          nq[x]++;
+        }
+        for (int j = 0; j < w.nj && ok; j++, gb++) {
+          const int s = gb % C::KST;
+          const uint32_t ph = ((gb / C::KST) & 1) ^ 1;
+          if (!mbar_wait(k_empty + 8 * s, ph, abort_sh, gflag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(k_full + 8 * s, C::TILE);
+          for (int c = 0; c < C::SUB; c++)
+            tma_load_3d(smem_u32(sK + s * C::TILE + c * SUB_BYTES), &tm_qkv, 64 * c, H + w.g,
+                        w.row0 + j * 128, k_full + 8 * s);
+          if (!mbar_wait(v_empty + 8 * s, ph, abort_sh, gflag)) {
+            ok = false;
+            drain_wait(k_full + 8 * s, ph ^ 1);
+            break;
+          }
+          mbar_arrive_expect_tx(v_full + 8 * s, C::TILE);
+          for (int c = 0; c < C::SUB; c++)
+            tma_load_3d(smem_u32(sV + s * C::TILE + c * SUB_BYTES), &tm_qkv, 64 * c, H + Hkv + w.g,
+                        w.row0 + j * 128, v_full + 8 * s);
+        }
+      }
+      // every copy this thread issued has landed before the CTA may exit
+      for (int x = 0; x < 2; x++)
+        for (int i = max(0, nq[x] - C::QS); i < nq[x]; i++)
+          drain_wait(q_full + 8 * (x * C::QS + i % C::QS), (i / C::QS) & 1);
+      for (int i = max(0, gb - C::KST); i < gb; i++) {
+        drain_wait(k_full + 8 * (i % C::KST), (i / C::KST) & 1);
+        drain_wait(v_full + 8 * (i % C::KST), (i / C::KST) & 1);
+      }
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ---------------------------------------- MMA issuer of stream x (whole warp)
+    const int x = warp - 1;
+    constexpr uint32_t ID_S = idesc_mn(128, 128, false, false);
+    constexpr uint32_t ID_O = idesc_mn(128, HD, false, true);
+    int gb = 0, nq = 0, cb = 0;  // the item's first ring block; Q tiles, blocks of the stream
+    bool ok = true;
+    auto wait = [&](uint32_t bar, int n) {  // the n-th phase of a barrier (n from 0)
+      ok = ok && warp_wait(bar, n & 1, abort_sh, gflag);
+      return ok;
+    };
+    for (int r = 0; ok; r++) {
+      const int item = sched_item(r, G, cta);
+      if (item >= n_items) break;
+      const Work w = work<HEADS>(pk, item, H, Hkv);
+      const int n = w.n[x];
+      const uint32_t qb = 8 * (x * C::QS + nq % C::QS);
+      const uint64_t qd = sdesc(smem_u32(sQ + (x * C::QS + nq % C::QS) * C::TILE), 16, 1024);
+      auto scores = [&](int j) {  // S = Q K_j^T
+        const int s = (gb + j) % C::KST;
+        if (!wait(k_full + 8 * s, (gb + j) / C::KST)) return;
+        fence_after();
+        const uint64_t kd = sdesc(smem_u32(sK + s * C::TILE), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; kk++) {
+          const uint64_t at = (uint64_t)((kk / 4) * (SUB_BYTES >> 4) + (kk % 4) * 2);
+          mma_bf16_e(tmem + C::S(x), qd + at, kd + at, ID_S, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_e(s_full + 8 * x);
+        mma_commit_e(k_empty + 8 * s);
+        if (j == n - 1) mma_commit_e(q_empty + qb);
+      };
+      if (n > 0) {
+        if (!wait(q_full + qb, nq / C::QS)) break;
+        // the buffer of the stream's previous block was read (P V done: P is in it)
+        if (cb > 0 && !wait((C::SEP ? s_free : o_done) + 8 * x, cb - 1)) break;
+        scores(0);
+        for (int j = 0; j < n && ok; j++, cb++) {
+          const int s = (gb + j) % C::KST;
+          if (C::SEP && j + 1 < n) {
+            if (!wait(s_free + 8 * x, cb)) break;
+            scores(j + 1);
+          }
+          if (!wait(v_full + 8 * s, (gb + j) / C::KST) || !wait(p_full + 8 * x, cb)) break;
+          fence_after();
+          const uint64_t vd = sdesc(smem_u32(sV + s * C::TILE), SUB_BYTES, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 8; kk++)
+            mma_ts_e(tmem + C::O(x), tmem + C::P(x) + kk * 8, vd + (uint64_t)(kk * 128), ID_O,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_e(o_done + 8 * x);
+          mma_commit_e(v_empty + 8 * s);
+          if (!C::SEP && j + 1 < n) {
+            if (!wait(o_done + 8 * x, cb)) break;
+            scores(j + 1);
+          }
+        }
+        nq++;
+      }
+      // key blocks that only the other stream reads: released once they are
+      // there, so that no arrival can count for an earlier use of the slot
+      for (int j = n; j < w.nj && ok; j++) {
+        const int s = (gb + j) % C::KST;
+        if (!wait(k_full + 8 * s, (gb + j) / C::KST)) break;
+        if (lane == 0) mbar_arrive(k_empty + 8 * s);
+        if (!wait(v_full + 8 * s, (gb + j) / C::KST)) break;
+        if (lane == 0) mbar_arrive(v_empty + 8 * s);
+      }
+      gb += w.nj;
+    }
+    mma_commit_e(drain + 8 * x);
+    if (lane == 0) drain_wait(drain + 8 * x, 0);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::S(x), tP = tmem + lane_off + C::P(x),
+                   tO = tmem + lane_off + C::O(x);
+    const float sl2 = scale * LOG2E;
+    int gb = 0, nq = 0, cb = 0;
+    bool ok = true;
+    for (int r = 0; ok; r++) {
+      const int item = sched_item(r, G, cta);
+      if (item >= n_items) break;
+      const Work w = work<HEADS>(pk, item, H, Hkv);
+      const int n = w.n[x], q0 = w.q[x] * 128, T = w.T;
+      if (n == 0) {
+        gb += w.nj;
+        continue;
+      }
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int j = 0; j < n; j++, cb++) {
+        if (!(ok = warp_wait(s_full + 8 * x, cb & 1, abort_sh, gflag))) break;
+        fence_after();
+        float sv[128];
+        {
+          uint32_t u[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; c++) tmem_ld_raw<32>(tS + 32 * c, u[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            tmem_after_wait(u[c]);
+#pragma unroll
+            for (int i = 0; i < 32; i++) sv[32 * c + i] = __uint_as_float(u[c][i]);
+          }
+        }
+        if constexpr (C::SEP) {  // the next block's scores may overwrite S
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + 8 * x);
+        }
+        const bool diag = j == n - 1;  // the row's own block: mask, and the sequence's end
+        if (diag) {
+          const int last = min(row, T - 1 - q0);  // keys up to the row itself
+#pragma unroll
+          for (int i = 0; i < 128; i++)
+            if (i > last) sv[i] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], sv[i], sv[i + 1]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        const bool need = top > m + LAZY;  // true on the first block with a key
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+          // O is rescaled after the product of the block before
+          if (!(ok = warp_wait(o_done + 8 * x, (cb - 1) & 1, abort_sh, gflag))) break;
+          fence_after();
+          const float corr = need ? ex2(m - top) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 16) {
+            float v[16];
+            uint32_t u[16];
+            tmem_ld16(tO + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; i++) u[i] = __float_as_uint(v[i] * corr);
+            tmem_st16(tO + c, u);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        if (need) {
+          const float corr = m == -INFINITY ? 0.f : ex2(m - top);
+          l2.x *= corr;
+          l2.y *= corr;
+          m = top;
+        }
+        const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          uint32_t pw[32];
+          if (diag) {  // on the SFU alone: masked scores give exact zeros
+            weights<false>(sv + 64 * c, sl2, mr, pw, l2);
+            weights<false>(sv + 64 * c + 32, sl2, mr, pw + 16, l2);
+          } else {
+            weights<true>(sv + 64 * c, sl2, mr, pw, l2);
+            weights<true>(sv + 64 * c + 32, sl2, mr, pw + 16, l2);
+          }
+          if (C::SEP && c == 0 && cb > 0) {  // P is free once the product before has read it
+            if (!(ok = warp_wait(o_done + 8 * x, (cb - 1) & 1, abort_sh, gflag))) break;
+            fence_after();
+          }
+          tmem_st32u(tP + 32 * c, pw);
+        }
+        if (!ok) break;
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        if (diag && q0 + 128 > T) {  // V rows past the sequence's end must be numbers
+          const int s = (gb + j) % C::KST;
+          if (!(ok = warp_wait(v_full + 8 * s, ((gb + j) / C::KST) & 1, abort_sh, gflag))) break;
+          if (q0 + row >= T) {
+#pragma unroll
+            for (int c = 0; c < C::SUB; c++) {
+              uint4 *p = reinterpret_cast<uint4 *>(sV + s * C::TILE + c * SUB_BYTES + row * 128);
+#pragma unroll
+              for (int i = 0; i < 8; i++) p[i] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * x);
+      }
+      if (!ok) break;
+      gb += w.nj;
+      // O = O / l: through the item's Q tile (its last S product is complete)
+      // in the 128-byte-swizzle image of the store's boxes
+      if (!(ok = warp_wait(o_done + 8 * x, (cb - 1) & 1, abort_sh, gflag))) break;
+      fence_after();
+      const float l = l2.x + l2.y, inv = 1.f / l;
+      uint8_t *tile = sQ + (x * C::QS + nq % C::QS) * C::TILE;
+#pragma unroll
+      for (int c = 0; c < HD / 32; c++) {
+        uint32_t u[32];
+        tmem_ld_raw<32>(tO + 32 * c, u);
+        tmem_wait_ld();
+        tmem_after_wait(u);
+        uint8_t *dst = tile + (c / 2) * SUB_BYTES + row * 128;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int ch = (c & 1) * 4 + i;
+          uint32_t pw[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            pw[e] = pack_bf16(__uint_as_float(u[8 * i + 2 * e]) * inv,
+                              __uint_as_float(u[8 * i + 2 * e + 1]) * inv);
+          *reinterpret_cast<uint4 *>(dst + ((ch ^ (row & 7)) << 4)) =
+              make_uint4(pw[0], pw[1], pw[2], pw[3]);
+        }
+      }
+      fence_before();
+      fence_proxy_async();
+      __syncwarp();
+      const int r0 = quarter * 32;  // the warp's rows: whole, or cut by the sequence's end
+      if (q0 + r0 + 32 <= T) {
+        if (lane == 0) {
+          for (int c = 0; c < C::SUB; c++)
+            tma_store_4d(&tm_o, smem_u32(tile + c * SUB_BYTES + r0 * 128), 64 * c, w.h[x],
+                         w.row0 + q0 + r0, 0);
+          bulk_commit();
+          bulk_wait_read();
+        }
+      } else {
+        for (int rr = r0; rr < r0 + 32; rr += 8)
+          for (int c = 0; c < C::SUB; c++)
+            store_cut(tile + c * SUB_BYTES, rr, T - q0,
+                      pk.out + (int64_t)(w.row0 + q0 + rr) * pk.out_ld + w.h[x] * hd + 64 * c,
+                      pk.out_ld, hd - 64 * c, lane);
+      }
+      if (q0 + row < T)
+        lse[w.h[x] * pk.n_rows + w.row0 + q0 + row] = (m + __log2f(l)) * LN2;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty + 8 * (x * C::QS + nq % C::QS));
+      nq++;
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+template <int HD, bool HEADS>
+static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag) {
+  auto kern = k_attn_fwd_pair<HD, HEADS>;
+  if (!smem_optin((const void *)kern, Cfg<HD>::SMEM)) return false;
+  const int64_t dw = (int64_t)a.H * a.hd;
+  CUtensorMap map, mo;
+  if (!head_map_load(&map, a.qkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, a.ld, 128) ||
+      !head_map_store(&mo, o, a.hd, a.H, a.n_rows, 1, dw, 32))
+    return false;
+  packed_plan(a, p, HEADS ? 128 : 256);
+  const int64_t items = p.cap * (HEADS ? a.H / 2 : a.H);
+  launch_dependent(kern, dim3((unsigned)(items < device_sms() ? items : device_sms())),
+                   dim3(NTHREADS), Cfg<HD>::SMEM, a.s, map, mo, lse, a.H, a.Hkv, a.hd,
+                   1.0f / sqrtf((float)a.hd),
+                   PkView{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)o, dw}, flag);
+  count_launch();
+  return true;
+}
+
+}  // namespace attn_pk_tc
+
+bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag) {
+  using namespace attn_pk_tc;
+  if (a.dt != DT_BF16 || (a.hd != 32 && a.hd != 64 && a.hd != 128)) return false;
+  const bool heads = (a.H / a.Hkv) % 2 == 0;
+  if (a.hd == 128)
+    return heads ? launch<128, true>(a, p, o, lse, flag) : launch<128, false>(a, p, o, lse, flag);
+  return heads ? launch<64, true>(a, p, o, lse, flag) : launch<64, false>(a, p, o, lse, flag);
+}
+
+}  // namespace llm

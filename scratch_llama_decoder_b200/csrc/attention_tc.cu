@@ -119,13 +119,9 @@ LLM_DEV bool softmax_all(bool v) {
 // Named barrier of the softmax warps (id 1).
 LLM_DEV void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * SM_WARPS) : "memory"); }
 
-// PK: the items are the tiles of a packed plan (pk) instead of B sequences of
-// T rows; T below is then the length of the item's own sequence.
-template <bool PK>
 __global__ void __launch_bounds__(NTHREADS, 1)
     k_attn_fwd_tc(const __grid_constant__ CUtensorMap tm_qkv, const __grid_constant__ CUtensorMap tm_o,
-                  float *__restrict__ lse, int B, int T_all, int H, int Hkv, int hd, float scale,
-                  const PkView pk, int *gflag) {
+                  float *__restrict__ lse, int B, int T, int H, int Hkv, float scale, int *gflag) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *sQ = smem, *sK = smem + QSLOTS * TILE_BYTES, *sV = sK + STAGES * TILE_BYTES;
@@ -147,15 +143,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   static_assert(2 * QSLOTS + 4 * STAGES + 4 + 3 * NQ + 2 <= 48,
                 "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int nqb = (T_all + BQ - 1) / BQ;
+  const int nqb = (T + BQ - 1) / BQ, n_items = nqb * H * B;
   const int G = gridDim.x, cta = blockIdx.x;
   // item -> (query block, head, batch): longest rows (last query blocks) first,
   // in bands of 4 query blocks taken pair by pair (band_item)
-  auto decode = [&](int item) {
-    if constexpr (PK) return pk_item(pk, item, H, false);
+  auto decode = [&](int item, int &qb, int &h, int &b) {
     int z, pr;
     band_item(item, nqb, H * B, z, pr);
-    return Item{nqb - 1 - z, pr % H, pr / H, pr / H * T_all, T_all};
+    qb = nqb - 1 - z;
+    h = pr % H;
+    b = pr / H;
   };
 
   if (threadIdx.x == 0) {
@@ -193,8 +190,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_sh;
-  if constexpr (PK) pk_wait();  // the plan comes from the kernel before
-  const int n_items = PK ? ld_int(pk.n_tiles) * H : nqb * H * B;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -204,9 +199,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int r = 0, it = 0; ok; r++, it++) {
         const int item = sched_item(r, G, cta);
         if (item >= n_items) break;
-        const Item im = decode(item);
-        const int qb = im.blk, h = im.h;
-        const int row_base = im.row0, g = h / (H / Hkv), slot = it % QSLOTS;
+        int qb, h, b;
+        decode(item, qb, h, b);
+        const int row_base = b * T, g = h / (H / Hkv), slot = it % QSLOTS;
         // Q into the slot of item it - QSLOTS once its last S product and the
         // store of its O (staged in the slot) completed
         if (!mbar_wait(q_empty + 8 * slot, ((it / QSLOTS) & 1) ^ 1, abort_sh, gflag)) break;
@@ -259,7 +254,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int gb = 0;
     int item = sched_item(0, G, cta);
     if (x == 0 && item < n_items) {  // scores of the first block
-      const int qb = decode(item).blk;
+      int qb, h, b;
+      decode(item, qb, h, b);
       ok = warp_wait(q_full, 0, abort_sh, gflag) && warp_wait(k_full, 0, abort_sh, gflag);
       if (ok) {
         fence_after();
@@ -268,9 +264,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     for (int r = 0, it = 0; item < n_items && ok; r++, it++) {
-      const int nj = decode(item).blk + 1, slot = it % QSLOTS;
+      int qb, h, b;
+      decode(item, qb, h, b);
+      const int nj = qb + 1, slot = it % QSLOTS;
       const int next = sched_item(r + 1, G, cta);
-      const int qb_next = next < n_items ? decode(next).blk : 0;
+      int qb_next = 0, hn, bn;
+      if (next < n_items) decode(next, qb_next, hn, bn);
       for (int j = 0; j < nj && ok; j++, gb++) {
         const int s = gb % STAGES;
         const uint32_t ph = (gb / STAGES) & 1;
@@ -341,8 +340,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int rr = 0, it = 0;; rr++, it++) {
       const int item = sched_item(rr, G, cta);
       if (item >= n_items) break;
-      const Item im = decode(item);
-      const int qb = im.blk, h = im.h, b = im.b, T = im.T;
+      int qb, h, b;
+      decode(item, qb, h, b);
       const int q0 = qb * BQ, nj = qb + 1;
       const int qi = q0 + r;
       float m_ref = -INFINITY, l = 0.f;
@@ -411,18 +410,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int c = 0; c < KW / 2; c += 16)
           tmem_stn<(KW / 2 < 16 ? KW / 2 : 16)>(tmem + lane_off + col_s + c, w + c);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        if constexpr (PK) {
-          // this group's V rows past the sequence's end take part with P = 0:
-          // they must be numbers
-          if (k0 + KW > T) {
-            const int s = gb % STAGES;
-            if (!warp_wait(v_full + 8 * s, (gb / STAGES) & 1, abort_sh, gflag)) {
-              ok = false;
-              break;
-            }
-            zero_rows(sV + s * TILE_BYTES + grp * KW * 128, T - k0, r);
-          }
-        }
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 8 * ((gb & 1) * NQ + grp));
@@ -498,24 +485,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // its part of O
       fence_before();
       softmax_sync();
-      // 8 whole rows of this warp's lane quarter (rows past T clipped; packed:
-      // the rows past a sequence's end are another's, so a cut piece leaves
-      // row by row)
-      const int r0 = quarter * 32 + grp * 8;
-      if (!PK || q0 + r0 + 8 <= T) {
-        if (lane == 0) {
-          tma_store_4d(&tm_o, smem_u32(sQ + (it % QSLOTS) * TILE_BYTES + r0 * 128), 0, h,
-                       PK ? im.row0 + q0 + r0 : q0 + r0, b);
-          bulk_commit();
-        }
-      } else {
-        store_cut(sQ + (it % QSLOTS) * TILE_BYTES, r0, T - q0,
-                  pk.out + (im.row0 + q0 + r0) * pk.out_ld + h * hd, pk.out_ld, hd, lane);
+      if (lane == 0) {  // 8 whole rows of this warp's lane quarter (rows past T clipped)
+        const int r0 = quarter * 32 + grp * 8;
+        tma_store_4d(&tm_o, smem_u32(sQ + (it % QSLOTS) * TILE_BYTES + r0 * 128), 0, h, q0 + r0, b);
+        bulk_commit();
       }
       st_slot = it % QSLOTS;  // released after the next item's first block
-      if (grp == 0 && qi < T)
-        lse[PK ? h * pk.n_rows + im.row0 + qi : ((int64_t)b * H + h) * T + qi] =
-            (m + __log2f(lt)) * LN2;
+      if (grp == 0 && qi < T) lse[((int64_t)b * H + h) * T + qi] = (m + __log2f(lt)) * LN2;
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -542,35 +518,15 @@ bool attn_fwd_tc(const void *qkv, void *o, float *lse, int B, int T, int H, int 
                  int *flag, cudaStream_t s) {
   using namespace attn_tc;
   if ((hd != 64 && hd != 32) || !flag) return false;
-  if (!smem_optin((const void *)k_attn_fwd_tc<false>, SMEM_BYTES)) return false;
+  if (!smem_optin((const void *)k_attn_fwd_tc, SMEM_BYTES)) return false;
   const int64_t qkvw = (int64_t)(H + 2 * Hkv) * hd;
   CUtensorMap map, mo;
   if (!head_map_load(&map, qkv, hd, H + 2 * Hkv, (int64_t)B * T, qkvw, 128) ||
       !head_map_store(&mo, o, hd, H, T, B, (int64_t)H * hd, 8))
     return false;
   const int items = ((T + BQ - 1) / BQ) * H * B;
-  k_attn_fwd_tc<false><<<min(items, device_sms()), NTHREADS, SMEM_BYTES, s>>>(
-      map, mo, lse, B, T, H, Hkv, hd, 1.0f / sqrtf((float)hd), PkView{}, flag);
-  count_launch();
-  return true;
-}
-
-// The same kernel over the tiles of a packed plan: one map over all rows (a
-// tile's rows past its sequence are loaded and masked), O through a map of
-// one batch of n_rows.
-bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag) {
-  using namespace attn_tc;
-  if (a.dt != DT_BF16 || (a.hd != 64 && a.hd != 32)) return false;
-  if (!smem_optin((const void *)k_attn_fwd_tc<true>, SMEM_BYTES)) return false;
-  const int64_t dw = (int64_t)a.H * a.hd;
-  CUtensorMap map, mo;
-  if (!head_map_load(&map, a.qkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, a.ld, 128) ||
-      !head_map_store(&mo, o, a.hd, a.H, a.n_rows, 1, dw, 8))
-    return false;
-  const int grid = (int)min(p.cap * a.H, (int64_t)device_sms());
-  launch_dependent(k_attn_fwd_tc<true>, dim3(grid), dim3(NTHREADS), SMEM_BYTES, a.s, map, mo, lse, 1,
-                   0, a.H, a.Hkv, a.hd, 1.0f / sqrtf((float)a.hd),
-                   PkView{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)o, dw}, flag);
+  k_attn_fwd_tc<<<min(items, device_sms()), NTHREADS, SMEM_BYTES, s>>>(
+      map, mo, lse, B, T, H, Hkv, 1.0f / sqrtf((float)hd), flag);
   count_launch();
   return true;
 }

@@ -1048,6 +1048,7 @@ bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float 
       !head_map_load(&mo, o, a.hd, a.H, a.n_rows, dw, 128) ||
       !head_map_store(&mst, dqkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, 1, dld, 8))
     return false;
+  packed_plan(a, p, PK_BLOCK);
   const int64_t sms = device_sms();
   const float scale = 1.0f / sqrtf((float)a.hd);
   const PkView pk{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)dqkv, dld};

@@ -12,7 +12,7 @@ constexpr int PK_MAX_SEQ = 65536;         // sequences of one call
 // bits OR-ed into the caller's flag word (FLAG_TIMEOUT is bit 4)
 enum : int { PK_BAD_OFFSETS = 1, PK_BAD_PAGE = 2 };
 
-// One 128-row tile of a sequence: first packed row and length of the
+// One tile of a sequence, 128 rows (or 256): first packed row and length of the
 // sequence, block index within it.  As a key tile the same entry stands for
 // block n - 1 - blk (n blocks), whose query blocks are as many.
 struct PkTile {
@@ -58,13 +58,15 @@ struct PkArgs {
   int *flag;  // device word, may be null
   cudaStream_t s;
 };
-void packed_plan(const PkArgs &a, const PkPlan &p);
-// tcgen05 kernels: bfloat16, head sizes 32 and 64, rows that start on 16
-// bytes; false (nothing launched) otherwise.  flag: non-null device word.
+// Enqueues the plan; block: rows of a tile, 128 or 256.
+void packed_plan(const PkArgs &a, const PkPlan &p, int block);
+// tcgen05 kernels (with their plan): bfloat16, head sizes 32, 64 and, forward,
+// 128, rows that start on 16 bytes; false (nothing launched) otherwise.  flag:
+// non-null device word.
 bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag);
 bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                    const void *dout, void *dqkv, int64_t dld, int *flag);
-// CUDA-core kernels: float32 arithmetic, either type, head sizes to 128.
+// CUDA-core kernels (with their plan): float32 arithmetic, either type, head sizes to 128.
 bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse);
 bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                      const void *dout, void *dqkv, int64_t dld);

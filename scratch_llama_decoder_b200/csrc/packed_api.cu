@@ -87,7 +87,6 @@ int llm_kernel_attention_packed_fwd(const void *d_qkv, int64_t ld, int dtype, co
     return LLM_ERR_ARG;
   if (!claim_device(nullptr)) return LLM_ERR_ARG;  // one device per process
   g_launches = 0;
-  packed_plan(a, p);
   int *flag = d_flag ? d_flag : p.n_tiles + 1;
   if (!packed_fwd_tc(a, p, d_o, d_lse, flag) && !packed_fwd_tile(a, p, d_o, d_lse))
     return LLM_ERR_CUDA;
@@ -113,7 +112,6 @@ int llm_kernel_attention_packed_bwd(const void *d_qkv, int64_t ld, int dtype, co
     return LLM_ERR_ARG;
   if (!claim_device(nullptr)) return LLM_ERR_ARG;
   g_launches = 0;
-  packed_plan(a, p);
   int *flag = d_flag ? d_flag : p.n_tiles + 1;
   if (!packed_bwd_tc(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld, flag) &&
       !packed_bwd_tile(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld))
