@@ -115,7 +115,10 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
     __syncthreads();
     carry = warp_tot[0];
   }
-  if (threadIdx.x == 0) *n_tiles = carry;
+  if (threadIdx.x == 0) {
+    n_tiles[0] = carry;
+    n_tiles[2] = 0;
+  }
   __syncthreads();
   for (int s = threadIdx.x >> 5; s < n_seq; s += PT / 32) {
     const int row0 = off[s], len = off[s + 1] - row0, n = (len + block - 1) / block;
@@ -172,7 +175,10 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
     base[c] = sum;
   }
   __syncthreads();
-  if (t == 0) *n_tiles = base[0];
+  if (t == 0) {
+    n_tiles[0] = base[0];
+    n_tiles[2] = 0;
+  }
   for (int s = t >> 5; s < n_seq; s += FEW / 32)
     for (int b = t & 31; b < blocks[s]; b += 32)
       tiles[base[b + 1] + rank[s]] = PkTile{off[s], off[s + 1] - off[s], b, 0};

@@ -9,14 +9,20 @@
 //   S = Q K_j^T         (M 128, N 128; operands K-major in shared memory)
 //   P = 2^(S c - m)     softmax: 4 warps, a thread holds one row whole
 //   O += P V_j          (M 128, N head size; A = P from TMEM, V MN-major)
-// While one stream's thread quadruple waits for its products, the other's
-// computes: the exponentials (the SFU gives 16 a clock and SM, a 128 x 128
-// block has 16384) bound the kernel, and one stream alone left the SFU idle
-// half the time (the one-tile kernel of the rectangular batch: 1900 cycles a
-// block).  A row per thread needs no exchange between threads: the running
-// maximum moves only when a block exceeds it by 2^8 (then the thread rescales
-// its own row of O in TMEM), and NP of every 16 pairs of exponentials run as a
-// polynomial on the FMA pipe (exp2_poly2).
+// While one stream's threads wait for their products, the other's compute.
+// The softmax bounds the kernel (1580 cycles a block and stream at 2 documents
+// of 16384 rows, heads 64; the products take 512): the SFU gives 16
+// exponentials a clock and SM, a block has 16384, of which NP of every 16
+// pairs run as a polynomial on the FMA pipe (exp2_poly2; 0, 2, 6 and 8 of 16
+// were 2 to 7% slower).  A row per thread needs no exchange between threads;
+// its running maximum moves only when a block exceeds it by 2^8, and the
+// thread then rescales its own row of O in TMEM.  Measured and dropped: two
+// threads a row (16 softmax warps, 13% slower on long sequences), the streams
+// taking turns at the exponentials (8%), weights formed on the old maximum
+// while the block's own is found (17%).
+// Items go to the CTAs from a queue, most work first (the plan clears its
+// counter); dealt in a fixed snake the fullest CTA had 6% more at 24 sequences
+// of 16001 rows in all.
 // TMEM: S_A, S_B (128 columns each), O_A, O_B (head size each).  Heads to 64
 // leave room for P beside S (SEP), so S_{j+1} is computed while block j's
 // softmax runs; at head 128 P takes the first half of S's columns, and S_{j+1}
@@ -37,6 +43,8 @@ using namespace attn_maps;
 
 constexpr int SUB_BYTES = 128 * 64 * 2;  // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int NTHREADS = 384;
+constexpr int SLOTS = 4;     // items handed out ahead
+constexpr int READERS = 10;  // warps that take items from the producer
 constexpr int TMEM_COLS = 512;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LAZY = 8.f;  // log2 units a row maximum may grow before O is rescaled
@@ -62,25 +70,24 @@ struct Work {
   int q[2], h[2];    // row block (of 128) and head of each stream
   int n[2], nj;      // key blocks of each stream (0: no rows), of the item
 };
+// t: the item's index and its tile (first row, length, block).
 template <bool HEADS>
-LLM_DEV Work work(const PkView &pk, int item, int H, int Hkv) {
-  const int heads = HEADS ? H / 2 : H, grp = H / Hkv;
-  const int4 t = ld_int4(pk.tiles + item / heads);
-  const int i = item % heads;
+LLM_DEV Work work(int4 t, int H, int Hkv) {
+  const int i = t.x % (HEADS ? H / 2 : H), grp = H / Hkv;
   Work w;
-  w.row0 = t.x;
-  w.T = t.y;
+  w.row0 = t.y;
+  w.T = t.z;
   if (HEADS) {
     w.h[0] = 2 * i;
     w.h[1] = 2 * i + 1;
-    w.q[0] = w.q[1] = t.z;
-    w.n[0] = w.n[1] = t.z + 1;
+    w.q[0] = w.q[1] = t.w;
+    w.n[0] = w.n[1] = t.w + 1;
   } else {
     w.h[0] = w.h[1] = i;
-    w.q[0] = 2 * t.z;
-    w.q[1] = 2 * t.z + 1;
-    w.n[0] = 2 * t.z + 1;
-    w.n[1] = w.q[1] * 128 < t.y ? 2 * t.z + 2 : 0;
+    w.q[0] = 2 * t.w;
+    w.q[1] = 2 * t.w + 1;
+    w.n[0] = 2 * t.w + 1;
+    w.n[1] = w.q[1] * 128 < t.z ? 2 * t.w + 2 : 0;
   }
   w.g = w.h[0] / grp;
   w.nj = max(w.n[0], w.n[1]);
@@ -127,15 +134,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t *bars = (uint64_t *)(sV + C::KST * C::TILE);
   uint32_t *tmem_sh = (uint32_t *)(bars + 48);
   volatile int *abort_sh = (volatile int *)(tmem_sh + 1);
+  int4 *items = (int4 *)(bars + 50);  // [SLOTS]
   const uint32_t b0 = smem_u32(bars);
   const uint32_t q_full = b0, q_empty = q_full + 16 * C::QS,  // [stream][slot]
                  k_full = q_empty + 16 * C::QS, k_empty = k_full + 8 * C::KST,
                  v_full = k_empty + 8 * C::KST, v_empty = v_full + 8 * C::KST,
                  s_full = v_empty + 8 * C::KST, s_free = s_full + 16, p_full = s_free + 16,
-                 o_done = p_full + 16, drain = o_done + 16;  // [stream] each
-  static_assert(4 * C::QS + 4 * C::KST + 10 <= 48, "barriers overlap the TMEM address word");
+                 o_done = p_full + 16, drain = o_done + 16,  // [stream] each
+                 i_full = drain + 16, i_empty = i_full + 8 * SLOTS;
+  static_assert(4 * C::QS + 4 * C::KST + 10 + 2 * SLOTS <= 48 && 400 + 16 * SLOTS <= BAR_BYTES,
+                "barriers overlap the TMEM address word or the items");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int G = gridDim.x, cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
     *abort_sh = 0;
@@ -156,6 +165,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(o_done + 8 * x, 1);
       mbar_init(drain + 8 * x, 1);
     }
+    for (int i = 0; i < SLOTS; i++) {
+      mbar_init(i_full + 8 * i, 1);
+      mbar_init(i_empty + 8 * i, READERS);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -170,17 +183,40 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   fence_after();
   const uint32_t tmem = *tmem_sh;
   pk_wait();  // the plan comes from the kernel before
-  const int n_items = ld_int(pk.n_tiles) * (HEADS ? H / 2 : H);
+  // The it-th item of this CTA, from the producer; t.x < 0: no more (or a wait
+  // gave up).  Whole warps; each takes every item once.
+  auto take = [&](int it) {
+    int4 t = make_int4(-1, 0, 0, 0);
+    const int sl = it % SLOTS;
+    if (warp_wait(i_full + 8 * sl, (it / SLOTS) & 1, abort_sh, gflag)) {
+      t = items[sl];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(i_empty + 8 * sl);
+    }
+    return t;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
       int gb = 0, nq[2] = {0, 0};  // key blocks, Q tiles of each stream issued
       bool ok = true;
-      for (int r = 0; ok; r++) {
-        const int item = sched_item(r, G, cta);
-        if (item >= n_items) break;
-        const Work w = work<HEADS>(pk, item, H, Hkv);
+      const int heads = HEADS ? H / 2 : H, n_items = ld_int(pk.n_tiles) * heads;
+      int item = blockIdx.x;
+      for (int it = 0;; it++) {
+        int4 t = make_int4(-1, 0, 0, 0);
+        if (item < n_items) {
+          const int4 u = ld_int4(pk.tiles + item / heads);
+          t = make_int4(item, u.x, u.y, u.z);
+        }
+        const int is = it % SLOTS;
+        if (!mbar_wait(i_empty + 8 * is, ((it / SLOTS) & 1) ^ 1, abort_sh, gflag)) break;
+        items[is] = t;
+        mbar_arrive(i_full + 8 * is);
+        if (t.x < 0) break;
+        // the next item, from the queue, while this one's tiles are loaded
+        item = gridDim.x + atomicAdd(pk.n_tiles + 2, 1);
+        const Work w = work<HEADS>(t, H, Hkv);
         for (int x = 0; x < 2 && ok; x++) {
           if (w.n[x] == 0) continue;
           const int sl = nq[x] % C::QS;
@@ -214,6 +250,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tma_load_3d(smem_u32(sV + s * C::TILE + c * SUB_BYTES), &tm_qkv, 64 * c, H + Hkv + w.g,
                         w.row0 + j * 128, v_full + 8 * s);
         }
+        if (!ok) break;
       }
       // every copy this thread issued has landed before the CTA may exit
       for (int x = 0; x < 2; x++)
@@ -235,10 +272,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       ok = ok && warp_wait(bar, n & 1, abort_sh, gflag);
       return ok;
     };
-    for (int r = 0; ok; r++) {
-      const int item = sched_item(r, G, cta);
-      if (item >= n_items) break;
-      const Work w = work<HEADS>(pk, item, H, Hkv);
+    for (int it = 0; ok; it++) {
+      const int4 t = take(it);
+      if (t.x < 0) break;
+      const Work w = work<HEADS>(t, H, Hkv);
       const int n = w.n[x];
       const uint32_t qb = 8 * (x * C::QS + nq % C::QS);
       const uint64_t qd = sdesc(smem_u32(sQ + (x * C::QS + nq % C::QS) * C::TILE), 16, 1024);
@@ -304,12 +341,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t tS = tmem + lane_off + C::S(x), tP = tmem + lane_off + C::P(x),
                    tO = tmem + lane_off + C::O(x);
     const float sl2 = scale * LOG2E;
-    int gb = 0, nq = 0, cb = 0;
+    int gb = 0, nq = 0, cb = 0, st_slot = -1;  // slot whose O store is still to be released
     bool ok = true;
-    for (int r = 0; ok; r++) {
-      const int item = sched_item(r, G, cta);
-      if (item >= n_items) break;
-      const Work w = work<HEADS>(pk, item, H, Hkv);
+    for (int it = 0; ok; it++) {
+      const int4 t = take(it);
+      if (t.x < 0) break;
+      const Work w = work<HEADS>(t, H, Hkv);
       const int n = w.n[x], q0 = w.q[x] * 128, T = w.T;
       if (n == 0) {
         gb += w.nj;
@@ -407,6 +444,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 8 * x);
+        if (st_slot >= 0) {  // the store of the item before has long read its tile
+          if (lane == 0) {
+            bulk_wait_read();
+            mbar_arrive(q_empty + 8 * (x * C::QS + st_slot));
+          }
+          st_slot = -1;
+        }
       }
       if (!ok) break;
       gb += w.nj;
@@ -415,7 +459,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!(ok = warp_wait(o_done + 8 * x, (cb - 1) & 1, abort_sh, gflag))) break;
       fence_after();
       const float l = l2.x + l2.y, inv = 1.f / l;
-      uint8_t *tile = sQ + (x * C::QS + nq % C::QS) * C::TILE;
+      const int sl = nq % C::QS;
+      uint8_t *tile = sQ + (x * C::QS + sl) * C::TILE;
 #pragma unroll
       for (int c = 0; c < HD / 32; c++) {
         uint32_t u[32];
@@ -445,7 +490,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tma_store_4d(&tm_o, smem_u32(tile + c * SUB_BYTES + r0 * 128), 64 * c, w.h[x],
                          w.row0 + q0 + r0, 0);
           bulk_commit();
-          bulk_wait_read();
         }
       } else {
         for (int rr = r0; rr < r0 + 32; rr += 8)
@@ -457,7 +501,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (q0 + row < T)
         lse[w.h[x] * pk.n_rows + w.row0 + q0 + row] = (m + __log2f(l)) * LN2;
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_empty + 8 * (x * C::QS + nq % C::QS));
+      if (C::QS > 1) {
+        st_slot = sl;  // released after the next item's first block
+      } else if (lane == 0) {  // the one slot is waited for
+        bulk_wait_read();
+        mbar_arrive(q_empty + 8 * (x * C::QS + sl));
+      }
       nq++;
     }
     if (lane == 0) bulk_wait_all();

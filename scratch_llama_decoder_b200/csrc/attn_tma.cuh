@@ -27,7 +27,7 @@ namespace attn_maps {
 // plan, the row count (stride of the heads in lse and D) and the output rows
 // for tiles that a sequence's end cuts.
 struct PkView {
-  const int *n_tiles;
+  int *n_tiles;  // [0] tiles of the plan, [2] counter of the queue
   const PkTile *tiles;
   int64_t n_rows;
   __nv_bfloat16 *out;

@@ -18,7 +18,8 @@ enum : int { PK_BAD_OFFSETS = 1, PK_BAD_PAGE = 2 };
 struct PkTile {
   int row0, len, blk, pad;
 };
-// The workspace: tile count (and a flag word for callers without one), then the tiles (most work first), then scratch
+// The workspace: tile count, a flag word for callers without one, the counter
+// of a queue of items (cleared by the plan); then the tiles (most work first), then scratch
 // of the plan (clamped offsets, ranks), then D of the backward.
 struct PkPlan {
   int *n_tiles;
@@ -38,7 +39,7 @@ inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward)
     at = (at + n + 255) / 256 * 256;
     return q;
   };
-  p.n_tiles = (int *)take(8);
+  p.n_tiles = (int *)take(12);
   p.tiles = (PkTile *)take(p.cap * (int64_t)sizeof(PkTile));
   p.off = (int *)take(4 * ((int64_t)n_seq + 1));
   p.rank = (int *)take(4 * (int64_t)n_seq);
