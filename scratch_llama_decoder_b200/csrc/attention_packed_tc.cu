@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_sh;
-  pk_wait();  // the plan comes from the kernel before
+  if (pk.tiles) pk_wait();  // the plan comes from the kernel before
   // The it-th item of this CTA, from the producer; t.x < 0: no more (or a wait
   // gave up).  Whole warps; each takes every item once.
   auto take = [&](int it) {
@@ -197,16 +197,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   };
 
   if (warp == 0) {
+    const int heads = HEADS ? H / 2 : H;
+    int4 only = make_int4(0, 0, 0, 0);
+    if (!pk.tiles)
+      only = pk_find(pk.cu, pk.n_seq, (int)pk.n_rows, HEADS ? 128 : 256, blockIdx.x / heads, gflag);
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
       int gb = 0, nq[2] = {0, 0};  // key blocks, Q tiles of each stream issued
       bool ok = true;
-      const int heads = HEADS ? H / 2 : H, n_items = ld_int(pk.n_tiles) * heads;
+      const int n_items = pk.tiles ? ld_int(pk.n_tiles) * heads : only.w * gridDim.x;
       int item = blockIdx.x;
       for (int it = 0;; it++) {
         int4 t = make_int4(-1, 0, 0, 0);
         if (item < n_items) {
-          const int4 u = ld_int4(pk.tiles + item / heads);
+          const int4 u = pk.tiles ? ld_int4(pk.tiles + item / heads) : only;
           t = make_int4(item, u.x, u.y, u.z);
         }
         const int is = it % SLOTS;
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_arrive(i_full + 8 * is);
         if (t.x < 0) break;
         // the next item, from the queue, while this one's tiles are loaded
-        item = gridDim.x + atomicAdd(pk.n_tiles + 2, 1);
+        item = pk.tiles ? gridDim.x + atomicAdd(pk.n_tiles + 2, 1) : n_items;
         const Work w = work<HEADS>(t, H, Hkv);
         for (int x = 0; x < 2 && ok; x++) {
           if (w.n[x] == 0) continue;
@@ -530,12 +534,21 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
   if (!head_map_load(&map, a.qkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, a.ld, 128) ||
       !head_map_store(&mo, o, a.hd, a.H, a.n_rows, 1, dw, 32))
     return false;
-  packed_plan(a, p, HEADS ? 128 : 256);
   const int64_t items = p.cap * (HEADS ? a.H / 2 : a.H);
-  launch_dependent(kern, dim3((unsigned)(items < device_sms() ? items : device_sms())),
-                   dim3(NTHREADS), Cfg<HD>::SMEM, a.s, map, mo, lse, a.H, a.Hkv, a.hd,
-                   1.0f / sqrtf((float)a.hd),
-                   PkView{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)o, dw}, flag);
+  // one item a block at most: no order to plan (17 rows, 8 heads: 10.3 us with
+  // the plan's kernel, 8.9 without)
+  const bool plan = items > device_sms() || a.n_seq > PK_FIND_SEQ;
+  const PkView pk{p.n_tiles, plan ? p.tiles : nullptr, a.n_rows, (__nv_bfloat16 *)o, dw, a.cu,
+                  a.n_seq};
+  const dim3 grid((unsigned)(items < device_sms() ? items : device_sms()));
+  if (plan) {
+    packed_plan(a, p, HEADS ? 128 : 256);
+    launch_dependent(kern, grid, dim3(NTHREADS), Cfg<HD>::SMEM, a.s, map, mo, lse, a.H, a.Hkv, a.hd,
+                     1.0f / sqrtf((float)a.hd), pk, flag);
+  } else {
+    kern<<<grid, NTHREADS, Cfg<HD>::SMEM, a.s>>>(map, mo, lse, a.H, a.Hkv, a.hd,
+                                                 1.0f / sqrtf((float)a.hd), pk, flag);
+  }
   count_launch();
   return true;
 }

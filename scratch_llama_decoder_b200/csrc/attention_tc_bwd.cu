@@ -177,12 +177,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  qred = qsync + 32;       // [4]: per lane quarter, its rows' D parts written
   static_assert(6 + 4 * STAGES + 18 <= 48, "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  __shared__ int4 only;  // a block's only tile, where there is no plan
   const int nqb = (T_all + BQ - 1) / BQ;
   const int G = gridDim.x, cta = blockIdx.x;
   // item -> (query block, head, batch): longest rows (last query blocks) first,
   // in bands of 4 query blocks taken pair by pair (band_item)
   auto decode = [&](int item) {
-    if constexpr (PK) return pk_item(pk, item, H, false);
+    if constexpr (PK) return pk_item(pk, only, item, H, false);
     int z, pr;
     band_item(item, nqb, H * B, z, pr);
     return Item{nqb - 1 - z, pr % H, pr / H, pr / H * T_all, T_all};
@@ -223,15 +224,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc_512(tmem_sh);
+  if constexpr (PK) {
+    if (warp == 0 && !pk.tiles) {
+      const int4 t = pk_find(pk.cu, pk.n_seq, (int)pk.n_rows, PK_BLOCK, blockIdx.x / H, gflag);
+      if (lane == 0) only = t;
+    }
+  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_sh;
   if constexpr (PK) {
     pk_release();
-    pk_wait();  // the plan comes from the kernel before
+    if (pk.tiles) pk_wait();  // the plan comes from the kernel before
   }
-  const int n_items = PK ? ld_int(pk.n_tiles) * H : nqb * H * B;
+  const int n_items =
+      PK ? (pk.tiles ? ld_int(pk.n_tiles) * H : only.w * (int)gridDim.x) : nqb * H * B;
 
   if (warp == 0) {
     // ---------------------------------------------- TMA producer (warp)
@@ -616,13 +624,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  qsync = drain + 16;   // [4]: per lane quarter, its rows of dK, dV staged
   static_assert(4 + 3 * STAGES + 10 <= 48, "barriers overlap the TMEM address word");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  __shared__ int4 only;  // a block's only tile, where there is no plan
   const int nkb_all = (T_all + BK - 1) / BK;
   const int G = gridDim.x, cta = blockIdx.x;
   const int grp = H / Hkv;
   // item -> (key block, kv head, batch), first key blocks first in bands of 4
   // taken pair by pair (band_item); steps = grp (nkb - kb)
   auto decode = [&](int item) {
-    if constexpr (PK) return pk_item(pk, item, Hkv, true);
+    if constexpr (PK) return pk_item(pk, only, item, Hkv, true);
     int kb, pr;
     band_item(item, nkb_all, Hkv * B, kb, pr);
     return Item{kb, pr % Hkv, pr / Hkv, pr / Hkv * T_all, T_all};
@@ -652,12 +661,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc_512(tmem_sh);
+  if constexpr (PK) {
+    if (warp == 0 && !pk.tiles) {
+      const int4 t = pk_find(pk.cu, pk.n_seq, (int)pk.n_rows, PK_BLOCK, blockIdx.x / Hkv, gflag);
+      if (lane == 0) only = t;
+    }
+  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_sh;
   if constexpr (PK) pk_wait();  // the plan, and D, come from the kernels before
-  const int n_items = PK ? ld_int(pk.n_tiles) * Hkv : nkb_all * Hkv * B;
+  const int n_items =
+      PK ? (pk.tiles ? ld_int(pk.n_tiles) * Hkv : only.w * (int)gridDim.x) : nkb_all * Hkv * B;
 
   if (warp == 0) {
     // ---------------------------------------------- TMA producer (warp)
@@ -1048,17 +1064,26 @@ bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float 
       !head_map_load(&mo, o, a.hd, a.H, a.n_rows, dw, 128) ||
       !head_map_store(&mst, dqkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, 1, dld, 8))
     return false;
-  packed_plan(a, p, PK_BLOCK);
   const int64_t sms = device_sms();
+  const bool plan = p.cap * a.H > sms || a.n_seq > PK_FIND_SEQ;  // as in the forward
   const float scale = 1.0f / sqrtf((float)a.hd);
-  const PkView pk{p.n_tiles, p.tiles, a.n_rows, (__nv_bfloat16 *)dqkv, dld};
+  const PkView pk{p.n_tiles, plan ? p.tiles : nullptr, a.n_rows, (__nv_bfloat16 *)dqkv, dld, a.cu,
+                  a.n_seq};
+  const dim3 gq((unsigned)min(p.cap * a.H, sms)), gkv((unsigned)min(p.cap * a.Hkv, sms));
   // L and D rows start anywhere: read by the lanes
-  launch_dependent(k_attn_dq_tc<true>, dim3((int)min(p.cap * a.H, sms)), dim3(NTHREADS), DQ_SMEM, a.s,
-                   mq, md, mo, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H,
-                   a.Hkv, a.hd, scale, 0, pk, flag);
-  launch_dependent(k_attn_dkv_tc<true>, dim3((int)min(p.cap * a.Hkv, sms)), dim3(NTHREADS), KV_SMEM,
-                   a.s, mq, md, mst, lse, p.D, (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H,
-                   a.Hkv, a.hd, scale, 0, pk, flag);
+  if (plan) {
+    packed_plan(a, p, PK_BLOCK);
+    launch_dependent(k_attn_dq_tc<true>, gq, dim3(NTHREADS), DQ_SMEM, a.s, mq, md, mo, mst, lse, p.D,
+                     (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H, a.Hkv, a.hd, scale, 0, pk,
+                     flag);
+  } else {
+    k_attn_dq_tc<true><<<gq, NTHREADS, DQ_SMEM, a.s>>>(mq, md, mo, mst, lse, p.D,
+                                                       (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1,
+                                                       0, a.H, a.Hkv, a.hd, scale, 0, pk, flag);
+  }
+  launch_dependent(k_attn_dkv_tc<true>, gkv, dim3(NTHREADS), KV_SMEM, a.s, mq, md, mst, lse, p.D,
+                   (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H, a.Hkv, a.hd, scale, 0, pk,
+                   flag);
   count_launch(2);
   return true;
 }

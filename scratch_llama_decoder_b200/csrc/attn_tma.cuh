@@ -32,13 +32,17 @@ struct PkView {
   int64_t n_rows;
   __nv_bfloat16 *out;
   int64_t out_ld;
+  // without a plan (tiles null): the offsets, one item a block
+  const int32_t *cu;
+  int n_seq;
 };
 // One work item: 128-row block (query or key), head, sequence.
 struct Item {
   int blk, h, b, row0, T;
 };
-LLM_DEV Item pk_item(const PkView &pk, int item, int heads, bool keys) {
-  const int4 t = ld_int4(pk.tiles + item / heads);
+// (tile: what pk_find gave, for a block's only item)
+LLM_DEV Item pk_item(const PkView &pk, const int4 &tile, int item, int heads, bool keys) {
+  const int4 t = pk.tiles ? ld_int4(pk.tiles + item / heads) : tile;
   const int n = (t.y + PK_BLOCK - 1) / PK_BLOCK;
   return Item{keys ? n - 1 - t.z : t.z, item % heads, 0, t.x, t.y};
 }

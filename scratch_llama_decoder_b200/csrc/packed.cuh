@@ -48,6 +48,44 @@ inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward)
   return p;
 }
 
+// Without a plan, where every block gets one item at most: tile k (in the
+// sequences' order) of `block` rows, found by a whole warp from the offsets
+// themselves, clamped as the plan clamps them.  {first row, length, block,
+// tile exists}.
+LLM_DEV int4 pk_find(const int32_t *cu, int n_seq, int n_rows, int block, int k, int *flag) {
+  const int lane = threadIdx.x & 31;
+  int top = 0;  // the largest offset so far
+  for (int s0 = 0; s0 < n_seq; s0 += 32) {
+    const int s = min(s0 + lane, n_seq - 1);
+    const int a = cu[s], b = cu[s + 1];
+    if (flag && (a < 0 || a > b || b > n_rows)) atomicOr(flag, PK_BAD_OFFSETS);
+    int lo = max(min(max(a, 0), n_rows), top), hi = min(max(b, 0), n_rows);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {  // lo = running maximum of the starts
+      const int t = __shfl_up_sync(0xffffffffu, lo, o);
+      if (lane >= o) lo = max(lo, t);
+    }
+    hi = max(hi, lo);
+    int n = s0 + lane < n_seq ? (hi - lo + block - 1) / block : 0;
+    const int own = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += t;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, k < n);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      return make_int4(__shfl_sync(0xffffffffu, lo, src), __shfl_sync(0xffffffffu, hi - lo, src),
+                       __shfl_sync(0xffffffffu, k - (n - own), src), 1);
+    }
+    k -= __shfl_sync(0xffffffffu, n, 31);
+    top = __shfl_sync(0xffffffffu, hi, 31);
+  }
+  return make_int4(0, 0, 0, 0);
+}
+constexpr int PK_FIND_SEQ = 256;  // sequences that a block looks through
+
 struct PkArgs {
   const void *qkv;
   int64_t ld;
