@@ -281,43 +281,16 @@ LLM_DEV float half_sum(float v) {
   for (int o = 1; o < 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Where the kernels find their tiles: a plan, or (tiles null) the offsets.
-struct Tiles {
-  const int *n_tiles;
-  const PkTile *tiles;
-  const int32_t *cu;
-  int n_seq, n_rows;
-  int *flag;
-};
-// Work item of a block: (tile, head, half of the tile's 128 rows).
-LLM_DEV bool item(const Tiles &w, int heads, PkTile &t, int &h, int &half) {
-  const int i = blockIdx.x >> 1, k = i / heads;
-  h = i % heads;
-  half = blockIdx.x & 1;
-  pk_release();
-  pk_wait();  // the plan, and D for dK/dV, come from the kernels before
-  int4 u;
-  if (w.tiles) {
-    if (k >= ld_int(w.n_tiles)) return false;
-    u = ld_int4(w.tiles + k);
-  } else {  // every warp for itself
-    u = pk_find(w.cu, w.n_seq, w.n_rows, PK_BLOCK, k, w.flag);
-    if (!u.w) return false;
-  }
-  t = PkTile{u.x, u.y, u.z, 0};
-  return true;
-}
-
 template <typename T, int HD>
 __global__ void __launch_bounds__(NT)
-    k_fwd(const T *__restrict__ qkv, int64_t ld, const Tiles tl, T *__restrict__ o, float *__restrict__ lse,
+    k_fwd(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, T *__restrict__ o, float *__restrict__ lse,
           int64_t n_rows, int H, int Hkv, int hd, bool vec) {
   extern __shared__ float4 sm4[];
   float *Qt = reinterpret_cast<float *>(sm4), *Kt = Qt + HD * TLD, *Vs = Kt + HD * TLD,
         *Pt = Vs + TB * HD;
   PkTile t;
   int h, half;
-  if (!item(tl, H, t, h, half)) return;
+  if (!pk_item64(tl, H, t, h, half)) return;
   const int q0 = t.blk * PK_BLOCK + half * TB;
   if (q0 >= t.len) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, g = h / (H / Hkv);
@@ -393,7 +366,7 @@ __global__ void __launch_bounds__(NT)
 // dQ, and D = rowsum(dO o O) for the dK/dV kernel.
 template <typename T, int HD>
 __global__ void __launch_bounds__(NT)
-    k_dq(const T *__restrict__ qkv, int64_t ld, const Tiles tl, const T *__restrict__ o, const float *__restrict__ lse,
+    k_dq(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, const T *__restrict__ o, const float *__restrict__ lse,
          const T *__restrict__ dout, float *__restrict__ D, T *__restrict__ dqkv, int64_t dld,
          int64_t n_rows, int H, int Hkv, int hd, bool vec) {
   extern __shared__ float4 sm4[];
@@ -401,7 +374,7 @@ __global__ void __launch_bounds__(NT)
         *Vt = Kt + HD * TLD, *Kr = Vt + HD * TLD, *dSt = Kr + TB * HD;
   PkTile t;
   int h, half;
-  if (!item(tl, H, t, h, half)) return;
+  if (!pk_item64(tl, H, t, h, half)) return;
   const int q0 = t.blk * PK_BLOCK + half * TB;
   if (q0 >= t.len) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, g = h / (H / Hkv);
@@ -472,7 +445,7 @@ __global__ void __launch_bounds__(NT)
 // the query tiles from the keys' own on.
 template <typename T, int HD>
 __global__ void __launch_bounds__(NT)
-    k_dkv(const T *__restrict__ qkv, int64_t ld, const Tiles tl, const float *__restrict__ lse,
+    k_dkv(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, const float *__restrict__ lse,
           const T *__restrict__ dout, const float *__restrict__ D, T *__restrict__ dqkv,
           int64_t dld, int64_t n_rows, int H, int Hkv, int hd, bool vec) {
   extern __shared__ float4 sm4[];
@@ -481,7 +454,7 @@ __global__ void __launch_bounds__(NT)
         *sL = Ps + TB * TB, *sD = sL + TB;
   PkTile t;
   int g, half;
-  if (!item(tl, Hkv, t, g, half)) return;
+  if (!pk_item64(tl, Hkv, t, g, half)) return;
   const int n = (t.len + PK_BLOCK - 1) / PK_BLOCK;
   const int k0 = (n - 1 - t.blk) * PK_BLOCK + half * TB;
   if (k0 >= t.len) return;
@@ -561,19 +534,12 @@ template <int HD> constexpr int dq_smem() { return (4 * HD * TLD + TB * HD + TB 
 template <int HD>
 constexpr int dkv_smem() { return (4 * HD * TLD + 2 * TB * HD + TB * TB + 2 * TB) * 4; }
 
-// No plan where all blocks run at once anyway.
-static bool planned(const PkArgs &a, const PkPlan &p) {
-  return 2 * p.cap * a.H > 2 * device_sms() || a.n_seq > PK_FIND_SEQ;
-}
-static Tiles tiles_of(const PkArgs &a, const PkPlan &p) {
-  return Tiles{p.n_tiles, planned(a, p) ? p.tiles : nullptr, a.cu, a.n_seq, (int)a.n_rows, a.flag};
-}
 template <typename T, int HD>
 static bool fwd(const PkArgs &a, const PkPlan &p, void *o, float *lse, bool vec) {
   if (!smem_optin((const void *)k_fwd<T, HD>, fwd_smem<HD>())) return false;
   launch_dependent(
       k_fwd<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(NT), fwd_smem<HD>(), a.s,
-      (const T *)a.qkv, a.ld, tiles_of(a, p), (T *)o, lse, a.n_rows, a.H, a.Hkv, a.hd, vec);
+      (const T *)a.qkv, a.ld, pk_tiles(a, p), (T *)o, lse, a.n_rows, a.H, a.Hkv, a.hd, vec);
   count_launch();
   return true;
 }
@@ -585,11 +551,11 @@ static bool bwd(const PkArgs &a, const PkPlan &p, const void *o, const float *ls
     return false;
   launch_dependent(
       k_dq<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(NT), dq_smem<HD>(), a.s,
-      (const T *)a.qkv, a.ld, tiles_of(a, p), (const T *)o, lse, (const T *)dout, p.D,
+      (const T *)a.qkv, a.ld, pk_tiles(a, p), (const T *)o, lse, (const T *)dout, p.D,
       (T *)dqkv, dld, a.n_rows, a.H, a.Hkv, a.hd, vec);
   launch_dependent(
       k_dkv<T, HD>, dim3((unsigned)(2 * p.cap * a.Hkv)), dim3(NT), dkv_smem<HD>(), a.s,
-      (const T *)a.qkv, a.ld, tiles_of(a, p), lse, (const T *)dout, p.D, (T *)dqkv, dld,
+      (const T *)a.qkv, a.ld, pk_tiles(a, p), lse, (const T *)dout, p.D, (T *)dqkv, dld,
       a.n_rows, a.H, a.Hkv, a.hd, vec);
   count_launch(2);
   return true;
@@ -616,7 +582,7 @@ void packed_plan(const PkArgs &a, const PkPlan &p, int block) {
 
 bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse) {
   using namespace pk;
-  if (planned(a, p)) packed_plan(a, p, PK_BLOCK);
+  if (pk_planned(a, p)) packed_plan(a, p, PK_BLOCK);
   const bool v = vec4(a, a.qkv);
   if (a.dt == DT_BF16) {
     using T = __nv_bfloat16;
@@ -631,7 +597,7 @@ bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse) {
 bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                      const void *dout, void *dqkv, int64_t dld) {
   using namespace pk;
-  if (planned(a, p)) packed_plan(a, p, PK_BLOCK);
+  if (pk_planned(a, p)) packed_plan(a, p, PK_BLOCK);
   const bool v = vec4(a, a.qkv) && vec4(a, dout);
   if (a.dt == DT_BF16) {
     using T = __nv_bfloat16;

@@ -1,5 +1,7 @@
-// tcgen05 flash attention over packed sequences, forward, head sizes 32, 64
-// and 128 (bf16 operands, fp32 softmax and accumulators).
+// tcgen05 flash attention over packed sequences, forward (bf16 operands, fp32
+// softmax and accumulators), for head sizes to 128 that are multiples of 8:
+// the tiles are 64 or 128 columns wide and zero past the head's own
+// (attn_tma.cuh).
 //
 // One CTA works on two 128-query tiles at once, streams A and B, that share
 // their key and value tiles: two query heads of one kv head at the same rows
@@ -557,9 +559,9 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
 
 bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag) {
   using namespace attn_pk_tc;
-  if (a.dt != DT_BF16 || (a.hd != 32 && a.hd != 64 && a.hd != 128)) return false;
+  if (a.dt != DT_BF16 || a.hd % 8) return false;
   const bool heads = (a.H / a.Hkv) % 2 == 0;
-  if (a.hd == 128)
+  if (a.hd > 64)
     return heads ? launch<128, true>(a, p, o, lse, flag) : launch<128, false>(a, p, o, lse, flag);
   return heads ? launch<64, true>(a, p, o, lse, flag) : launch<64, false>(a, p, o, lse, flag);
 }

@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       fence_after();
       // column pairs (c, c + hd/2) of RoPE: this group takes c in [xc, xc + HW)
       // (head 32: groups 2 and 3 repeat 0 and 1 and stage nothing)
-      const int half = hd / 2, xc = (hd == 64 ? cq : (cq & 1)) * HW;
+      const int half = PK ? HD / 2 : hd / 2, xc = (PK || hd == 64 ? cq : (cq & 1)) * HW;
       float xa[HW], ya[HW], xb[HW], yb[HW];
       {  // the four loads in flight together, one wait
         uint32_t ra[HW], rya[HW], rb[HW], ryb[HW];
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // 128-byte-swizzle image of the tile, then each warp stores 8 whole rows
       // of its lane quarter with one bulk tensor copy (rows past T clipped)
       uint8_t *srow = sQ + slot * TILE_BYTES + r * 128;
-      if (hd == 64 || cq < 2) {
+      if (PK || hd == 64 || cq < 2) {
         stage_n<HW>(srow, xc / 8, r, xa, scale);
         stage_n<HW>(srow, (half + xc) / 8, r, ya, scale);
       }
@@ -948,7 +948,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // column pairs (c, c + hd/2) of RoPE in dK: this group takes c in
       // [xc, xc + HW) (head 32: groups 2 and 3 repeat 0 and 1 and stage no dK);
       // dV: columns [cq HW, cq HW + HW) and 32 more (zero past head 32)
-      const int half = hd / 2, xc = (hd == 64 ? cq : (cq & 1)) * HW;
+      const int half = PK ? HD / 2 : hd / 2, xc = (PK || hd == 64 ? cq : (cq & 1)) * HW;
       float xk[HW], yk[HW], xv[HW], yv[HW];
       {  // the four loads in flight together, one wait
         uint32_t rk[HW], ryk[HW], rv[HW], ryv[HW];
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // complete), then each warp stores 8 whole rows of its lane quarter of
       // both with bulk tensor copies (rows past T clipped)
       uint8_t *rk = sK + slot * TILE_BYTES + r * 128, *rv = sV + slot * TILE_BYTES + r * 128;
-      if (hd == 64 || cq < 2) {
+      if (PK || hd == 64 || cq < 2) {
         stage_n<HW>(rk, xc / 8, r, xk, scale);
         stage_n<HW>(rk, (half + xc) / 8, r, yk, scale);
       }
@@ -1053,7 +1053,7 @@ bool attn_bwd_tc(const void *qkv, const void *o, const void *dout, const float *
 bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                    const void *dout, void *dqkv, int64_t dld, int *flag) {
   using namespace attn_tc_bwd;
-  if (a.dt != DT_BF16 || (a.hd != 64 && a.hd != 32)) return false;
+  if (a.dt != DT_BF16 || a.hd % 8 || a.hd > 64) return false;
   if (!smem_optin((const void *)k_attn_dq_tc<true>, DQ_SMEM) ||
       !smem_optin((const void *)k_attn_dkv_tc<true>, KV_SMEM))
     return false;

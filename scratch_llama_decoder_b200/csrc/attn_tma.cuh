@@ -9,8 +9,8 @@
 // head's 32 values, which lie outside the tensor's innermost extent: a load
 // fills them with zeros (so Q K^T, P V, dO V^T and the row sums dO . O are
 // the head-32 values, and the products' columns 32..63 are zero) and a store
-// skips them (only the head's own 32 columns are written).  For hd = 128 (the
-// packed forward) a head is two boxes.
+// skips them (only the head's own 32 columns are written).  The
+// packed kernels take any multiple of 8 so (past 64, forward, as two boxes).
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -159,7 +159,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 inline bool head_map_load(CUtensorMap *map, const void *base, int hd, int64_t heads, int64_t rows,
                           int64_t ld, int box_rows) {
   auto encode = encoder();
-  if (!encode || ((uintptr_t)base & 15) || (hd != 32 && hd != 64 && hd != 128) || ld < heads * hd || ld % 8)
+  if (!encode || ((uintptr_t)base & 15) || hd < 8 || hd > 128 || hd % 8 || ld < heads * hd || ld % 8)
     return false;
   cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2};
@@ -176,7 +176,7 @@ inline bool head_map_load(CUtensorMap *map, const void *base, int hd, int64_t he
 inline bool head_map_store(CUtensorMap *map, void *base, int hd, int64_t heads, int64_t T,
                            int64_t batches, int64_t ld, int box_rows) {
   auto encode = encoder();
-  if (!encode || ((uintptr_t)base & 15) || (hd != 32 && hd != 64 && hd != 128) || ld < heads * hd || ld % 8)
+  if (!encode || ((uintptr_t)base & 15) || hd < 8 || hd > 128 || hd % 8 || ld < heads * hd || ld % 8)
     return false;
   cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)batches};
   cuuint64_t strides[3] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2, (cuuint64_t)(ld * T * 2)};

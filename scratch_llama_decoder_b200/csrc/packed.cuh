@@ -97,14 +97,53 @@ struct PkArgs {
   int *flag;  // device word, may be null
   cudaStream_t s;
 };
+// Where the kernels of 64-row blocks find their tiles: a plan, or (tiles null) the offsets.
+struct PkTiles {
+  const int *n_tiles;
+  const PkTile *tiles;
+  const int32_t *cu;
+  int n_seq, n_rows;
+  int *flag;
+};
+// Work item of a block: (tile, head, half of the tile's 128 rows).
+LLM_DEV bool pk_item64(const PkTiles &w, int heads, PkTile &t, int &h, int &half) {
+  const int i = blockIdx.x >> 1, k = i / heads;
+  h = i % heads;
+  half = blockIdx.x & 1;
+  pk_release();
+  pk_wait();  // the plan, and D for dK/dV, come from the kernels before
+  int4 u;
+  if (w.tiles) {
+    if (k >= ld_int(w.n_tiles)) return false;
+    u = ld_int4(w.tiles + k);
+  } else {  // every warp for itself
+    u = pk_find(w.cu, w.n_seq, w.n_rows, PK_BLOCK, k, w.flag);
+    if (!u.w) return false;
+  }
+  t = PkTile{u.x, u.y, u.z, 0};
+  return true;
+}
+
+// No plan where all blocks run at once anyway.
+inline bool pk_planned(const PkArgs &a, const PkPlan &p) {
+  return 2 * p.cap * a.H > 2 * device_sms() || a.n_seq > PK_FIND_SEQ;
+}
+inline PkTiles pk_tiles(const PkArgs &a, const PkPlan &p) {
+  return PkTiles{p.n_tiles, pk_planned(a, p) ? p.tiles : nullptr, a.cu, a.n_seq, (int)a.n_rows, a.flag};
+}
 // Enqueues the plan; block: rows of a tile, 128 or 256.
 void packed_plan(const PkArgs &a, const PkPlan &p, int block);
-// tcgen05 kernels (with their plan): bfloat16, head sizes 32, 64 and, forward,
-// 128, rows that start on 16 bytes; false (nothing launched) otherwise.  flag:
+// tcgen05 kernels (with their plan): bfloat16, head sizes that are multiples of
+// 8 (to 128 forward, to 64 backward), rows that start on 16 bytes; false
+// (nothing launched) otherwise.  flag:
 // non-null device word.
 bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag);
 bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                    const void *dout, void *dqkv, int64_t dld, int *flag);
+// mma.sync kernels (with their plan): the backward of bfloat16 head sizes to
+// 128, as above.
+bool packed_bwd_mma(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
+                    const void *dout, void *dqkv, int64_t dld);
 // CUDA-core kernels (with their plan): float32 arithmetic, either type, head sizes to 128.
 bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse);
 bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,

@@ -114,6 +114,7 @@ int llm_kernel_attention_packed_bwd(const void *d_qkv, int64_t ld, int dtype, co
   g_launches = 0;
   int *flag = d_flag ? d_flag : p.n_tiles + 1;
   if (!packed_bwd_tc(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld, flag) &&
+      !packed_bwd_mma(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld) &&
       !packed_bwd_tile(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld))
     return LLM_ERR_CUDA;
   return launched();
