@@ -185,15 +185,31 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
 }
 
 // --------------------------------------------------------- CUDA-core kernels
-// 64 x 64 tiles in shared memory, 256 threads (tx, ty) of 4 x 4 scores each.
-// Operands of a score product sit transposed ([column][row], rows padded by
-// 4), operands of an accumulation row by row; a probability tile as
-// [column][row] float4 slots, slot ty of column k at ty ^ (k / 4), so that a
-// half-warp's float4 stores fall on different banks.  Head columns past hd
-// are zero, so a head size runs on the next of 32, 64, 128.
-constexpr int TB = 64, TLD = TB + 4, NT = 256;
+// 64 x 64 tiles, R x 4 results a thread (R = 8, or 4 at head 128 where the
+// gradients' accumulators leave no room), 16 x 64 / R threads: tx = thread %
+// 16, ty = thread / 16.  A thread's rows of a product are R ty .. R ty + R - 1
+// of one tile, its columns rows tx + 16 c of the other; both are read along
+// the head as float4 from tiles that lie row by row (padded by 4, so that the
+// 16 tx fall on different banks), 12 loads to 128 multiply-adds at R = 8, two
+// to an instruction (f32x2).  So no tile is transposed and float32 rows come
+// by cp.async.  A tile of weights lies [row][column], the columns of odd ty
+// with bit 4 turned (both ty of a warp would store to the same banks).  Head
+// columns past hd are zero, so a head size runs on the next of 32, 64, 128.
+// Against 4 x 4 results a thread from transposed tiles: training step of
+// 16384 rows, 4 heads of 32, 538 -> 400 us.
+constexpr int TB = 64, LDP = TB + 4;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+// 2^x, the SFU's instruction alone (relative error 2^-22): exp2f adds the
+// scaling of subnormal results, which no weight needs.
+LLM_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int HD> constexpr int rows_of() { return HD == 128 ? 4 : 8; }
+template <int HD> constexpr int threads_of() { return 16 * TB / rows_of<HD>(); }
+template <int HD> constexpr int tile_of() { return TB * (HD + 4); }  // floats
 
-LLM_DEV int slot(int k, int g4) { return k * TB + ((g4 ^ (k >> 2)) & 15) * 4; }
 // Output column c of a thread: float4 groups 64 columns apart (head 128), so
 // that the 16 threads of a row read consecutive float4.
 template <int HD>
@@ -216,59 +232,96 @@ LLM_DEV float4 read4(const __nv_bfloat16 *p, bool vec, int n) {
   return make_float4(n > 0 ? to_f(p[0]) : 0.f, n > 1 ? to_f(p[1]) : 0.f,
                      n > 2 ? to_f(p[2]) : 0.f, n > 3 ? to_f(p[3]) : 0.f);
 }
-// Rows [0, nrows) of src (row stride ld), hd columns, times mul: transposed
-// into At and/or row by row into Mr; the other rows read as 0.
+// Rows [0, nrows) of src (row stride ld), hd columns, into a tile; the rest 0.
+// float32 rows of whole float4 by cp.async (the caller waits).
 template <typename T, int HD>
-LLM_DEV void load_tile(const T *src, int64_t ld, int nrows, int hd, bool vec, float mul, float *At,
-                       float *Mr) {
-  for (int i = threadIdx.x; i < TB * HD / 4; i += NT) {
-    const int row = i % TB, c = i / TB * 4;
-    float4 v = row < nrows && c < hd ? read4(src + row * ld + c, vec, hd - c)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-    v.x *= mul; v.y *= mul; v.z *= mul; v.w *= mul;
-    if (At) {
-      At[(c + 0) * TLD + row] = v.x;
-      At[(c + 1) * TLD + row] = v.y;
-      At[(c + 2) * TLD + row] = v.z;
-      At[(c + 3) * TLD + row] = v.w;
-    }
-    if (Mr) *reinterpret_cast<float4 *>(Mr + row * HD + c) = v;
-  }
-}
-template <int HD>
-LLM_DEV void dot(const float *At, const float *Bt, int tx, int ty, float (&acc)[4][4]) {
-#pragma unroll 8
-  for (int e = 0; e < HD; e++) {
-    const float4 a = *reinterpret_cast<const float4 *>(At + e * TLD + ty * 4);
-    const float4 b = *reinterpret_cast<const float4 *>(Bt + e * TLD + tx * 4);
-    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int r = 0; r < 4; r++)
-#pragma unroll
-      for (int c = 0; c < 4; c++) acc[r][c] = fmaf(av[r], bv[c], acc[r][c]);
-  }
-}
-template <int HD>
-LLM_DEV void accumulate(const float *P, const float *M, int tx, int ty, float (&out)[4][HD / 16]) {
-#pragma unroll 4
-  for (int k = 0; k < TB; k++) {
-    const float4 p = *reinterpret_cast<const float4 *>(P + slot(k, ty));
-    const float pv[4] = {p.x, p.y, p.z, p.w};
-    float mv[HD / 16];
-    if constexpr (HD == 32) {
-      const float2 m = *reinterpret_cast<const float2 *>(M + k * HD + tx * 2);
-      mv[0] = m.x; mv[1] = m.y;
+LLM_DEV void load_tile(float *t, const T *src, int64_t ld, int nrows, int hd, bool vec) {
+  for (int i = threadIdx.x; i < TB * HD / 4; i += threads_of<HD>()) {
+    const int row = i / (HD / 4), c = i % (HD / 4) * 4;
+    float *dst = t + row * (HD + 4) + c;
+    const bool in = row < nrows && c < hd;
+    if (sizeof(T) == 4 && vec) {  // vec: hd is a multiple of 4
+      const T *p = in ? src + row * ld + c : src;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(dst)),
+                   "l"(p), "r"(in ? 16 : 0)
+                   : "memory");
     } else {
+      *reinterpret_cast<float4 *>(dst) =
+          in ? read4(src + row * ld + c, vec, hd - c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+}
+LLM_DEV void tiles_ready() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+}
+// s[r][c] = A[R ty + r] . B[tx + 16 c]
+template <int HD, int R>
+LLM_DEV void dot(const float *A, const float *B, int tx, int ty, float (&s)[R][4]) {
+  float2 acc[R][4];
 #pragma unroll
-      for (int c = 0; c < HD / 16; c += 4) {
-        const float4 m = *reinterpret_cast<const float4 *>(M + k * HD + out_col<HD>(tx, c));
-        mv[c] = m.x; mv[c + 1] = m.y; mv[c + 2] = m.z; mv[c + 3] = m.w;
+  for (int r = 0; r < R; r++)
+#pragma unroll
+    for (int c = 0; c < 4; c++) acc[r][c] = make_float2(0.f, 0.f);
+#pragma unroll 2
+  for (int e = 0; e < HD; e += 4) {
+    float4 b[4];
+#pragma unroll
+    for (int c = 0; c < 4; c++)
+      b[c] = *reinterpret_cast<const float4 *>(B + (tx + 16 * c) * (HD + 4) + e);
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const float4 a = *reinterpret_cast<const float4 *>(A + (R * ty + r) * (HD + 4) + e);
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        acc[r][c] = __ffma2_rn(make_float2(a.x, a.y), make_float2(b[c].x, b[c].y), acc[r][c]);
+        acc[r][c] = __ffma2_rn(make_float2(a.z, a.w), make_float2(b[c].z, b[c].w), acc[r][c]);
       }
     }
+  }
 #pragma unroll
-    for (int r = 0; r < 4; r++)
+  for (int r = 0; r < R; r++)
 #pragma unroll
-      for (int c = 0; c < HD / 16; c++) out[r][c] = fmaf(pv[r], mv[c], out[r][c]);
+    for (int c = 0; c < 4; c++) s[r][c] = acc[r][c].x + acc[r][c].y;
+}
+template <int R>
+LLM_DEV void put(float *P, const float (&p)[R][4], int tx, int ty) {
+#pragma unroll
+  for (int r = 0; r < R; r++)
+#pragma unroll
+    for (int c = 0; c < 4; c++) P[(R * ty + r) * LDP + ((tx + 16 * c) ^ ((ty & 1) * 16))] = p[r][c];
+}
+// out[r][c] += sum_k P[R ty + r][k] M[k][out_col(c)]
+template <int HD, int R>
+LLM_DEV void accumulate(const float *P, const float *M, int tx, int ty, float (&out)[R][HD / 16]) {
+#pragma unroll 2
+  for (int k = 0; k < TB; k += 4) {
+    float4 p[R];
+#pragma unroll
+    for (int r = 0; r < R; r++)
+      p[r] = *reinterpret_cast<const float4 *>(P + (R * ty + r) * LDP + (k ^ ((ty & 1) * 16)));
+#pragma unroll
+    for (int kk = 0; kk < 4; kk++) {
+      float mv[HD / 16];
+      const float *m = M + (k + kk) * (HD + 4);
+      if constexpr (HD == 32) {
+        const float2 v = *reinterpret_cast<const float2 *>(m + tx * 2);
+        mv[0] = v.x; mv[1] = v.y;
+      } else {
+#pragma unroll
+        for (int c = 0; c < HD / 16; c += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(m + out_col<HD>(tx, c));
+          mv[c] = v.x; mv[c + 1] = v.y; mv[c + 2] = v.z; mv[c + 3] = v.w;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        const float w = kk == 0 ? p[r].x : kk == 1 ? p[r].y : kk == 2 ? p[r].z : p[r].w;
+#pragma unroll
+        for (int c = 0; c < HD / 16; c++) out[r][c] = fmaf(w, mv[c], out[r][c]);
+      }
+    }
   }
 }
 LLM_DEV float half_max(float v) {
@@ -282,96 +335,93 @@ LLM_DEV float half_sum(float v) {
   return v;
 }
 template <typename T, int HD>
-__global__ void __launch_bounds__(NT)
-    k_fwd(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, T *__restrict__ o, float *__restrict__ lse,
-          int64_t n_rows, int H, int Hkv, int hd, bool vec) {
+LLM_DEV void put_row(T *dst, const float (&v)[HD / 16], float mul, int tx, int hd) {
+#pragma unroll
+  for (int c = 0; c < HD / 16; c++) {
+    const int e = out_col<HD>(tx, c);
+    if (e < hd) dst[e] = from_f<T>(v[c] * mul);
+  }
+}
+
+// Shared memory: Q, K, V, P.
+template <typename T, int HD>
+__global__ void __launch_bounds__(threads_of<HD>())
+    k_fwd(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, T *__restrict__ o,
+          float *__restrict__ lse, int64_t n_rows, int H, int Hkv, int hd, bool vec) {
+  constexpr int R = rows_of<HD>();
   extern __shared__ float4 sm4[];
-  float *Qt = reinterpret_cast<float *>(sm4), *Kt = Qt + HD * TLD, *Vs = Kt + HD * TLD,
-        *Pt = Vs + TB * HD;
+  float *Q = reinterpret_cast<float *>(sm4), *K = Q + tile_of<HD>(), *V = K + tile_of<HD>(),
+        *P = V + tile_of<HD>();
   PkTile t;
   int h, half;
   if (!pk_item64(tl, H, t, h, half)) return;
   const int q0 = t.blk * PK_BLOCK + half * TB;
   if (q0 >= t.len) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, g = h / (H / Hkv);
+  const float sl2 = LOG2E / sqrtf((float)hd);
   const T *base = qkv + (int64_t)t.row0 * ld;
   const T *kcol = base + (int64_t)(H + g) * hd, *vcol = base + (int64_t)(H + Hkv + g) * hd;
-  load_tile<T, HD>(base + q0 * ld + (int64_t)h * hd, ld, min(TB, t.len - q0), hd, vec,
-                   1.0f / sqrtf((float)hd), Qt, nullptr);
-  float m[4], l[4], acc[4][HD / 16];
+  load_tile<T, HD>(Q, base + q0 * ld + (int64_t)h * hd, ld, min(TB, t.len - q0), hd, vec);
+  float m[R], l[R], acc[R][HD / 16];
 #pragma unroll
-  for (int r = 0; r < 4; r++) {
+  for (int r = 0; r < R; r++) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
     for (int c = 0; c < HD / 16; c++) acc[r][c] = 0.f;
   }
   for (int k0 = 0; k0 <= q0; k0 += TB) {
-    __syncthreads();  // the previous tile's products are done with Kt, Vs and Pt
+    __syncthreads();  // the previous tile's products are done with K, V and P
     const int nk = min(TB, t.len - k0);
-    load_tile<T, HD>(kcol + k0 * ld, ld, nk, hd, vec, 1.f, Kt, nullptr);
-    load_tile<T, HD>(vcol + k0 * ld, ld, nk, hd, vec, 1.f, nullptr, Vs);
-    __syncthreads();
-    float s[4][4] = {};
-    dot<HD>(Qt, Kt, tx, ty, s);
-    if (k0 == q0) {
+    load_tile<T, HD>(K, kcol + k0 * ld, ld, nk, hd, vec);
+    load_tile<T, HD>(V, vcol + k0 * ld, ld, nk, hd, vec);
+    tiles_ready();
+    float s[R][4];
+    dot<HD, R>(Q, K, tx, ty, s);
 #pragma unroll
-      for (int r = 0; r < 4; r++)
+    for (int r = 0; r < R; r++) {
 #pragma unroll
-        for (int c = 0; c < 4; c++)
-          if (tx * 4 + c > ty * 4 + r) s[r][c] = -INFINITY;
-    }
-    float p[4][4];
-#pragma unroll
-    for (int r = 0; r < 4; r++) {
+      for (int c = 0; c < 4; c++) {
+        s[r][c] *= sl2;
+        if (k0 == q0 && tx + 16 * c > R * ty + r) s[r][c] = -INFINITY;
+      }
       const float mn =
           fmaxf(m[r], half_max(fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]))));
       // a row whose scores are all -inf so far keeps the sums it has (0)
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float corr = expf(m[r] - ref);
-      float ps = 0.f;
+      const float ref = mn == -INFINITY ? 0.f : mn, corr = ex2(m[r] - ref);
 #pragma unroll
-      for (int c = 0; c < 4; c++) {
-        p[c][r] = expf(s[r][c] - ref);
-        ps += p[c][r];
-      }
-      l[r] = l[r] * corr + ps;
+      for (int c = 0; c < 4; c++) s[r][c] = ex2(s[r][c] - ref);
+      l[r] = l[r] * corr + ((s[r][0] + s[r][1]) + (s[r][2] + s[r][3]));
       m[r] = mn;
 #pragma unroll
       for (int c = 0; c < HD / 16; c++) acc[r][c] *= corr;
     }
-#pragma unroll
-    for (int c = 0; c < 4; c++)
-      *reinterpret_cast<float4 *>(Pt + slot(tx * 4 + c, ty)) =
-          make_float4(p[c][0], p[c][1], p[c][2], p[c][3]);
+    put<R>(P, s, tx, ty);
     __syncthreads();
-    accumulate<HD>(Pt, Vs, tx, ty, acc);
+    accumulate<HD, R>(P, V, tx, ty, acc);
   }
 #pragma unroll
-  for (int r = 0; r < 4; r++) {
+  for (int r = 0; r < R; r++) {
     const float lt = half_sum(l[r]);
-    const int q = q0 + ty * 4 + r;
+    const int q = q0 + R * ty + r;
     if (q >= t.len) continue;
     const int64_t row = (int64_t)t.row0 + q;
-    T *orow = o + row * ((int64_t)H * hd) + (int64_t)h * hd;
-#pragma unroll
-    for (int c = 0; c < HD / 16; c++) {
-      const int e = out_col<HD>(tx, c);
-      if (e < hd) orow[e] = from_f<T>(acc[r][c] / lt);
-    }
-    if (tx == 0) lse[(int64_t)h * n_rows + row] = m[r] + logf(lt);
+    put_row<T, HD>(o + row * ((int64_t)H * hd) + (int64_t)h * hd, acc[r], 1.f / lt, tx, hd);
+    if (tx == 0) lse[(int64_t)h * n_rows + row] = (m[r] + log2f(lt)) * LN2;
   }
 }
 
-// dQ, and D = rowsum(dO o O) for the dK/dV kernel.
+// dQ, and D = rowsum(dO o O) for the dK/dV kernel.  Shared memory: Q, dO, K,
+// V, dS.
 template <typename T, int HD>
-__global__ void __launch_bounds__(NT)
-    k_dq(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, const T *__restrict__ o, const float *__restrict__ lse,
-         const T *__restrict__ dout, float *__restrict__ D, T *__restrict__ dqkv, int64_t dld,
-         int64_t n_rows, int H, int Hkv, int hd, bool vec) {
+__global__ void __launch_bounds__(threads_of<HD>())
+    k_dq(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, const T *__restrict__ o,
+         const float *__restrict__ lse, const T *__restrict__ dout, float *__restrict__ D,
+         T *__restrict__ dqkv, int64_t dld, int64_t n_rows, int H, int Hkv, int hd, bool vec) {
+  constexpr int R = rows_of<HD>();
   extern __shared__ float4 sm4[];
-  float *Qt = reinterpret_cast<float *>(sm4), *dOt = Qt + HD * TLD, *Kt = dOt + HD * TLD,
-        *Vt = Kt + HD * TLD, *Kr = Vt + HD * TLD, *dSt = Kr + TB * HD;
+  float *Q = reinterpret_cast<float *>(sm4), *G = Q + tile_of<HD>(), *K = G + tile_of<HD>(),
+        *V = K + tile_of<HD>(), *S = V + tile_of<HD>();
   PkTile t;
   int h, half;
   if (!pk_item64(tl, H, t, h, half)) return;
@@ -380,25 +430,26 @@ __global__ void __launch_bounds__(NT)
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, g = h / (H / Hkv);
   const int nq = min(TB, t.len - q0);
   const int64_t ow = (int64_t)H * hd;
-  const float scale = 1.0f / sqrtf((float)hd);
+  const float scale = 1.0f / sqrtf((float)hd), sl2 = scale * LOG2E;
   const T *base = qkv + (int64_t)t.row0 * ld;
   const T *kcol = base + (int64_t)(H + g) * hd, *vcol = base + (int64_t)(H + Hkv + g) * hd;
   const int64_t orow0 = ((int64_t)t.row0 + q0) * ow + (int64_t)h * hd;
-  load_tile<T, HD>(base + q0 * ld + (int64_t)h * hd, ld, nq, hd, vec, scale, Qt, nullptr);
-  load_tile<T, HD>(dout + orow0, ow, nq, hd, vec, 1.f, dOt, nullptr);
-  float Dr[4], Lr[4], dq[4][HD / 16];
+  load_tile<T, HD>(Q, base + q0 * ld + (int64_t)h * hd, ld, nq, hd, vec);
+  load_tile<T, HD>(G, dout + orow0, ow, nq, hd, vec);
+  float Dr[R], Lr[R], dq[R][HD / 16];
 #pragma unroll
-  for (int r = 0; r < 4; r++) {
-    const int q = ty * 4 + r;
+  for (int r = 0; r < R; r++) {
+    const int q = R * ty + r;
     float part = 0.f;
     if (q < nq)
+#pragma unroll
       for (int c = 0; c < HD / 16; c++) {
         const int e = out_col<HD>(tx, c);
         if (e < hd) part += to_f(o[orow0 + q * ow + e]) * to_f(dout[orow0 + q * ow + e]);
       }
     Dr[r] = half_sum(part);
     const int64_t li = (int64_t)h * n_rows + t.row0 + q0 + q;
-    Lr[r] = q < nq ? lse[li] : INFINITY;  // rows past the sequence: P = 0
+    Lr[r] = q < nq ? lse[li] * LOG2E : INFINITY;  // rows past the sequence: P = 0
     if (tx == 0 && q < nq) D[li] = Dr[r];
 #pragma unroll
     for (int c = 0; c < HD / 16; c++) dq[r][c] = 0.f;
@@ -406,52 +457,43 @@ __global__ void __launch_bounds__(NT)
   for (int k0 = 0; k0 <= q0; k0 += TB) {
     __syncthreads();
     const int nk = min(TB, t.len - k0);
-    load_tile<T, HD>(kcol + k0 * ld, ld, nk, hd, vec, 1.f, Kt, Kr);
-    load_tile<T, HD>(vcol + k0 * ld, ld, nk, hd, vec, 1.f, Vt, nullptr);
-    __syncthreads();
-    float s[4][4] = {}, dp[4][4] = {};
-    dot<HD>(Qt, Kt, tx, ty, s);
-    dot<HD>(dOt, Vt, tx, ty, dp);
-    float ds[4][4];
+    load_tile<T, HD>(K, kcol + k0 * ld, ld, nk, hd, vec);
+    load_tile<T, HD>(V, vcol + k0 * ld, ld, nk, hd, vec);
+    tiles_ready();
+    float s[R][4], dp[R][4];
+    dot<HD, R>(Q, K, tx, ty, s);
+    dot<HD, R>(G, V, tx, ty, dp);
 #pragma unroll
-    for (int r = 0; r < 4; r++)
+    for (int r = 0; r < R; r++)
 #pragma unroll
       for (int c = 0; c < 4; c++) {
-        const bool masked = k0 == q0 && tx * 4 + c > ty * 4 + r;
-        const float p = expf(s[r][c] - Lr[r]);
-        ds[c][r] = masked ? 0.f : p * (dp[r][c] - Dr[r]);
+        const bool masked = k0 == q0 && tx + 16 * c > R * ty + r;
+        const float p = ex2(s[r][c] * sl2 - Lr[r]);
+        s[r][c] = masked ? 0.f : p * (dp[r][c] - Dr[r]);
       }
-#pragma unroll
-    for (int c = 0; c < 4; c++)
-      *reinterpret_cast<float4 *>(dSt + slot(tx * 4 + c, ty)) =
-          make_float4(ds[c][0], ds[c][1], ds[c][2], ds[c][3]);
+    put<R>(S, s, tx, ty);
     __syncthreads();
-    accumulate<HD>(dSt, Kr, tx, ty, dq);
+    accumulate<HD, R>(S, K, tx, ty, dq);
   }
 #pragma unroll
-  for (int r = 0; r < 4; r++) {
-    const int q = ty * 4 + r;
-    if (q >= nq) continue;
-    T *dst = dqkv + ((int64_t)t.row0 + q0 + q) * dld + (int64_t)h * hd;
-#pragma unroll
-    for (int c = 0; c < HD / 16; c++) {
-      const int e = out_col<HD>(tx, c);
-      if (e < hd) dst[e] = from_f<T>(dq[r][c] * scale);
-    }
-  }
+  for (int r = 0; r < R; r++)
+    if (R * ty + r < nq)
+      put_row<T, HD>(dqkv + ((int64_t)t.row0 + q0 + R * ty + r) * dld + (int64_t)h * hd, dq[r],
+                     scale, tx, hd);
 }
 
 // dK, dV of 64 keys: the query heads of the kv head in order, and for each
-// the query tiles from the keys' own on.
+// the query tiles from the keys' own on.  Shared memory: K, V, Q, dO, a tile
+// that holds P, then dS, and L and D of the queries.
 template <typename T, int HD>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(threads_of<HD>())
     k_dkv(const T *__restrict__ qkv, int64_t ld, const PkTiles tl, const float *__restrict__ lse,
           const T *__restrict__ dout, const float *__restrict__ D, T *__restrict__ dqkv,
           int64_t dld, int64_t n_rows, int H, int Hkv, int hd, bool vec) {
+  constexpr int R = rows_of<HD>();
   extern __shared__ float4 sm4[];
-  float *Kt = reinterpret_cast<float *>(sm4), *Vt = Kt + HD * TLD, *Qt = Vt + HD * TLD,
-        *dOt = Qt + HD * TLD, *Qr = dOt + HD * TLD, *dOr = Qr + TB * HD, *Ps = dOr + TB * HD,
-        *sL = Ps + TB * TB, *sD = sL + TB;
+  float *K = reinterpret_cast<float *>(sm4), *V = K + tile_of<HD>(), *Q = V + tile_of<HD>(),
+        *G = Q + tile_of<HD>(), *P = G + tile_of<HD>(), *sL = P + TB * LDP, *sD = sL + TB;
   PkTile t;
   int g, half;
   if (!pk_item64(tl, Hkv, t, g, half)) return;
@@ -461,84 +503,70 @@ __global__ void __launch_bounds__(NT)
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, grp = H / Hkv;
   const int nk = min(TB, t.len - k0);
   const int64_t ow = (int64_t)H * hd;
-  const float scale = 1.0f / sqrtf((float)hd);
+  const float scale = 1.0f / sqrtf((float)hd), sl2 = scale * LOG2E;
   const T *base = qkv + (int64_t)t.row0 * ld;
   const T *kcol = base + (int64_t)(H + g) * hd, *vcol = base + (int64_t)(H + Hkv + g) * hd;
-  load_tile<T, HD>(kcol + k0 * ld, ld, nk, hd, vec, 1.f, Kt, nullptr);
-  load_tile<T, HD>(vcol + k0 * ld, ld, nk, hd, vec, 1.f, Vt, nullptr);
-  float dk[4][HD / 16], dv[4][HD / 16];
+  load_tile<T, HD>(K, kcol + k0 * ld, ld, nk, hd, vec);
+  load_tile<T, HD>(V, vcol + k0 * ld, ld, nk, hd, vec);
+  float dk[R][HD / 16], dv[R][HD / 16];
 #pragma unroll
-  for (int r = 0; r < 4; r++)
+  for (int r = 0; r < R; r++)
 #pragma unroll
     for (int c = 0; c < HD / 16; c++) dk[r][c] = dv[r][c] = 0.f;
   for (int h = g * grp; h < (g + 1) * grp; h++) {
     for (int q0 = k0; q0 < t.len; q0 += TB) {
       __syncthreads();
       const int nq = min(TB, t.len - q0);
-      load_tile<T, HD>(base + q0 * ld + (int64_t)h * hd, ld, nq, hd, vec, scale, Qt, Qr);
-      load_tile<T, HD>(dout + ((int64_t)t.row0 + q0) * ow + (int64_t)h * hd, ow, nq, hd, vec, 1.f,
-                       dOt, dOr);
+      load_tile<T, HD>(Q, base + q0 * ld + (int64_t)h * hd, ld, nq, hd, vec);
+      load_tile<T, HD>(G, dout + ((int64_t)t.row0 + q0) * ow + (int64_t)h * hd, ow, nq, hd, vec);
       if (threadIdx.x < TB) {
         const int64_t li = (int64_t)h * n_rows + t.row0 + q0 + threadIdx.x;
         const bool in = (int)threadIdx.x < nq;
-        sL[threadIdx.x] = in ? lse[li] : INFINITY;  // queries past the sequence: P = 0
+        sL[threadIdx.x] = in ? lse[li] * LOG2E : INFINITY;  // past the sequence: P = 0
         sD[threadIdx.x] = in ? ld_float(D + li) : 0.f;
       }
-      __syncthreads();
-      float s[4][4] = {}, dp[4][4] = {};
-      dot<HD>(Kt, Qt, tx, ty, s);  // rows keys, columns queries
-      dot<HD>(Vt, dOt, tx, ty, dp);
-      float p[4][4], ds[4][4];
+      tiles_ready();
+      float s[R][4], dp[R][4];
+      dot<HD, R>(K, Q, tx, ty, s);  // rows keys, columns queries
+      dot<HD, R>(V, G, tx, ty, dp);
 #pragma unroll
-      for (int r = 0; r < 4; r++)
+      for (int c = 0; c < 4; c++) {
+        const float L = sL[tx + 16 * c], d = sD[tx + 16 * c];
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          const bool masked = q0 == k0 && ty * 4 + r > tx * 4 + c;
-          const float e = masked ? 0.f : expf(s[r][c] - sL[tx * 4 + c]);
-          p[c][r] = e;
-          ds[c][r] = masked ? 0.f : e * (dp[r][c] - sD[tx * 4 + c]);
+        for (int r = 0; r < R; r++) {
+          const bool masked = q0 == k0 && R * ty + r > tx + 16 * c;
+          const float e = masked ? 0.f : ex2(s[r][c] * sl2 - L);
+          s[r][c] = e;
+          dp[r][c] = masked ? 0.f : e * (dp[r][c] - d);
         }
-#pragma unroll
-      for (int c = 0; c < 4; c++)
-        *reinterpret_cast<float4 *>(Ps + slot(tx * 4 + c, ty)) =
-            make_float4(p[c][0], p[c][1], p[c][2], p[c][3]);
+      }
+      put<R>(P, s, tx, ty);
       __syncthreads();
-      accumulate<HD>(Ps, dOr, tx, ty, dv);
-      __syncthreads();  // one tile holds P, then dS: head 128 has no room for both
-#pragma unroll
-      for (int c = 0; c < 4; c++)
-        *reinterpret_cast<float4 *>(Ps + slot(tx * 4 + c, ty)) =
-            make_float4(ds[c][0], ds[c][1], ds[c][2], ds[c][3]);
+      accumulate<HD, R>(P, G, tx, ty, dv);
+      __syncthreads();  // one tile holds P, then dS
+      put<R>(P, dp, tx, ty);
       __syncthreads();
-      accumulate<HD>(Ps, Qr, tx, ty, dk);  // Qr holds q / sqrt(hd)
+      accumulate<HD, R>(P, Q, tx, ty, dk);
     }
   }
 #pragma unroll
-  for (int r = 0; r < 4; r++) {
-    if (ty * 4 + r >= nk) continue;
-    T *dkr = dqkv + ((int64_t)t.row0 + k0 + ty * 4 + r) * dld + (int64_t)(H + g) * hd;
-    T *dvr = dkr + (int64_t)Hkv * hd;
-#pragma unroll
-    for (int c = 0; c < HD / 16; c++) {
-      const int e = out_col<HD>(tx, c);
-      if (e < hd) {
-        dkr[e] = from_f<T>(dk[r][c]);
-        dvr[e] = from_f<T>(dv[r][c]);
-      }
-    }
+  for (int r = 0; r < R; r++) {
+    if (R * ty + r >= nk) continue;
+    T *dst = dqkv + ((int64_t)t.row0 + k0 + R * ty + r) * dld + (int64_t)(H + g) * hd;
+    put_row<T, HD>(dst, dk[r], scale, tx, hd);
+    put_row<T, HD>(dst + (int64_t)Hkv * hd, dv[r], 1.f, tx, hd);
   }
 }
 
-template <int HD> constexpr int fwd_smem() { return (2 * HD * TLD + TB * HD + TB * TB) * 4; }
-template <int HD> constexpr int dq_smem() { return (4 * HD * TLD + TB * HD + TB * TB) * 4; }
-template <int HD>
-constexpr int dkv_smem() { return (4 * HD * TLD + 2 * TB * HD + TB * TB + 2 * TB) * 4; }
+template <int HD> constexpr int fwd_smem() { return (3 * tile_of<HD>() + TB * LDP) * 4; }
+template <int HD> constexpr int dq_smem() { return (4 * tile_of<HD>() + TB * LDP) * 4; }
+template <int HD> constexpr int dkv_smem() { return (4 * tile_of<HD>() + TB * LDP + 2 * TB) * 4; }
 
 template <typename T, int HD>
 static bool fwd(const PkArgs &a, const PkPlan &p, void *o, float *lse, bool vec) {
   if (!smem_optin((const void *)k_fwd<T, HD>, fwd_smem<HD>())) return false;
   launch_dependent(
-      k_fwd<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(NT), fwd_smem<HD>(), a.s,
+      k_fwd<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(threads_of<HD>()), fwd_smem<HD>(), a.s,
       (const T *)a.qkv, a.ld, pk_tiles(a, p), (T *)o, lse, a.n_rows, a.H, a.Hkv, a.hd, vec);
   count_launch();
   return true;
@@ -550,11 +578,11 @@ static bool bwd(const PkArgs &a, const PkPlan &p, const void *o, const float *ls
       !smem_optin((const void *)k_dkv<T, HD>, dkv_smem<HD>()))
     return false;
   launch_dependent(
-      k_dq<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(NT), dq_smem<HD>(), a.s,
+      k_dq<T, HD>, dim3((unsigned)(2 * p.cap * a.H)), dim3(threads_of<HD>()), dq_smem<HD>(), a.s,
       (const T *)a.qkv, a.ld, pk_tiles(a, p), (const T *)o, lse, (const T *)dout, p.D,
       (T *)dqkv, dld, a.n_rows, a.H, a.Hkv, a.hd, vec);
   launch_dependent(
-      k_dkv<T, HD>, dim3((unsigned)(2 * p.cap * a.Hkv)), dim3(NT), dkv_smem<HD>(), a.s,
+      k_dkv<T, HD>, dim3((unsigned)(2 * p.cap * a.Hkv)), dim3(threads_of<HD>()), dkv_smem<HD>(), a.s,
       (const T *)a.qkv, a.ld, pk_tiles(a, p), lse, (const T *)dout, p.D, (T *)dqkv, dld,
       a.n_rows, a.H, a.Hkv, a.hd, vec);
   count_launch(2);

@@ -121,49 +121,67 @@ LLM_DEV void kv_read8(const uint8_t *pages, int64_t elem, bool vec, int n, float
   }
 }
 
-// The scale of a row whose largest magnitude is amax.
+// The scale of a row whose largest magnitude has the bits `top` (a NaN's are
+// above an infinity's), and its reciprocal.
 //   e4m3: the least power of two s with amax <= 448 s (s >= 2^-126), so that
-//     x / s and code * s are exact and the code is x / s rounded once;
+//     x / s and code * s are exact and the code is x / s rounded once: 448 is
+//     1.75 * 2^8, so the exponent is amax's less 8, or 7 past mantissa 1.75;
 //   int8: amax / 127 rounded to float32 (at least the least normal number).
 // A row that holds an infinity or a NaN has a NaN scale: it reads back as
 // NaN instead of as finite values.
 template <int FMT>
-LLM_DEV float row_scale(float amax) {
-  if (!(amax < INFINITY)) return __uint_as_float(0x7fc00000u);
+LLM_DEV float row_scale(uint32_t top, float *inv) {
+  const bool bad = top >= 0x7f800000u;
   if constexpr (FMT == KV_E4M3) {
-    // amax / 448 <= 2^e: the exponent of the quotient, one more unless it is
-    // a power of two itself.  The quotient is rounded up, so that amax <= 448 s
-    // holds for the amax next above a power of two times 448, too.
-    const uint32_t u = __float_as_uint(__fdiv_ru(amax, 448.f));
-    const int e = (int)(u >> 23) - 127 + ((u & 0x7fffffu) ? 1 : 0);
-    return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
+    const int f = max((int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), 1);
+    *inv = __uint_as_float((uint32_t)(254 - f) << 23);
+    return bad ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)f << 23);
   } else {
-    return fmaxf(__fdiv_rn(amax, 127.f), 1.17549435e-38f);
+    const float s = fmaxf(__fdiv_rn(__uint_as_float(top), 127.f), 1.17549435e-38f);
+    *inv = __fdividef(1.f, s);  // to a few units: encode8 does not rely on it
+    return bad ? __uint_as_float(0x7fc00000u) : s;
   }
 }
-// x / scale to the nearest code, ties to even.
+// x / scale to the nearest code, ties to even, for 8 elements.
 template <int FMT>
-LLM_DEV uint32_t encode4(const float *x, float scale, float inv) {
-  if constexpr (FMT == KV_E4M3) {  // inv = 1 / scale, exact
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    return lo | hi << 16;
-  } else {
-    // q = x / scale in float32 may land on the wrong side of a border between
-    // two codes; the remainder r = x - q scale (one rounding, exact where it
-    // decides) puts the code right: 2 |r| <= scale, and even on the border
-    uint32_t w = 0;
+LLM_DEV void encode8(const float (&x)[8], float scale, float inv, uint32_t (&c)[2]) {
+  if constexpr (FMT == KV_E4M3) {  // inv is exact
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      float q = rintf(x[i] * inv);
-      const float r2 = 2.f * fmaf(-q, scale, x[i]);
-      if (r2 > scale || (r2 == scale && ((int)q & 1))) q += 1.f;
-      else if (r2 < -scale || (r2 == -scale && ((int)q & 1))) q -= 1.f;
-      w |= ((uint32_t)(int)fminf(fmaxf(q, -127.f), 127.f) & 0xffu) << (8 * i);
+    for (int w = 0; w < 2; w++) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+          make_float2(x[4 * w] * inv, x[4 * w + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+          make_float2(x[4 * w + 2] * inv, x[4 * w + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+      c[w] = lo | hi << 16;
     }
-    return w;
+  } else {
+    // q = x inv rounded to an integer by adding 1.5 * 2^23, whose low bits then
+    // hold it.  inv is not exact, so q may lie on the wrong side of a border
+    // between two codes; the remainder r = x - q scale (one rounding, exact
+    // where it decides) tells: |2 r| < scale, or the element is looked at again.
+    constexpr float MAGIC = 12582912.f;
+    uint32_t t[8];
+    bool close = false;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const float m = fmaf(x[i], inv, MAGIC), q = m - MAGIC;
+      t[i] = __float_as_uint(m);
+      close |= fabsf(2.f * fmaf(-q, scale, x[i])) >= scale;
+    }
+    if (close) {  // on a border or past it by the rounding of inv: even, or the next
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        float q = (float)(int8_t)(t[i] & 0xff);
+        const float r2 = 2.f * fmaf(-q, scale, x[i]);
+        if (r2 > scale || (r2 == scale && (t[i] & 1))) q += 1.f;
+        else if (r2 < -scale || (r2 == -scale && (t[i] & 1))) q -= 1.f;
+        t[i] = (uint32_t)(int)q;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; w++)
+      c[w] = __byte_perm(__byte_perm(t[4 * w], t[4 * w + 1], 0x0040),
+                         __byte_perm(t[4 * w + 2], t[4 * w + 3], 0x0040), 0x5410);
   }
 }
 
@@ -177,98 +195,132 @@ LLM_DEV int seq_of(const int32_t *cu, int n_seq, int64_t i) {
   }
   return lo >= 1 && lo <= n_seq && cu[lo - 1] <= i ? lo - 1 : -1;
 }
-// The cache row of packed row i, -1 when it has none.
+// ------------------------------------------------------------ write and read
+// A block takes 32 packed rows.  One warp looks their places up (a chain of
+// dependent loads: search, table) while the others have the rows' first loads
+// in flight.  Then a warp takes 32 / LPH rows, LPH lanes of 8 elements each,
+// and walks through their heads, a few at a time: a row's heads lie together
+// where they are packed, and a head's rows, with their scales, in its page.
+// Bound by memory, and next to it by instructions: 16001 rows of 16 heads of
+// 64, bfloat16 to e4m3 (101 MB): write 23 us (4.3 TB/s), read 26.  (A warp per
+// packed row, scattered 64-byte pieces: 39 and 26; rows and heads of a step
+// found by division: 57 and 44.)
+constexpr int RW_ROWS = 32, RW_THREADS = 256, RW_HEADS = 8;
+constexpr int WU = 4, RU = 2;  // heads in flight: write, read (read with 4: 31 us)
+constexpr int64_t NO_PLACE = -1, NO_SEQUENCE = -2;
 LLM_DEV int64_t place(const KvView &kv, const int32_t *cu, const int32_t *start, int n_seq,
-                      int64_t i, int *seq) {
+                      int64_t i) {
   const int s = seq_of(cu, n_seq, i);
-  *seq = s;
-  if (s < 0) return -1;
+  if (s < 0) return NO_SEQUENCE;
   const int64_t row = kv_row(kv, s, (start ? (int64_t)start[s] : 0) + i - cu[s]);
-  if (row < 0 && kv.flag && (threadIdx.x & 31) == 0) atomicOr(kv.flag, PK_BAD_PAGE);
-  return row;
+  if (row < 0 && kv.flag) atomicOr(kv.flag, PK_BAD_PAGE);
+  return row < 0 ? NO_PLACE : row;
 }
 
-// ------------------------------------------------------------------- write
-// One warp per packed row: its k and v heads in groups of lanes, 8 elements a
-// lane, so that a head's largest magnitude is a few shuffles away.
-constexpr int RW_THREADS = 256;
-template <typename T, int FMT>
+template <typename T, int FMT, int LPH, bool VEC>
 __global__ void __launch_bounds__(RW_THREADS)
     k_write(const KvView kv, const T *__restrict__ qkv, int64_t ld, const int32_t *__restrict__ cu,
-            const int32_t *__restrict__ start, int n_seq, int64_t n_rows, int H, int lph,
-            bool vec) {
-  const int64_t i = blockIdx.x * (int64_t)(RW_THREADS / 32) + threadIdx.x / 32;
-  if (i >= n_rows) return;
-  int s;
-  const int64_t row = place(kv, cu, start, n_seq, i, &s);
-  if (row < 0) return;
-  const int lane = threadIdx.x & 31, sub = lane % lph, e = sub * 8;
-  const T *src = qkv + i * ld + (int64_t)H * kv.hd;  // k heads, then v heads
-  for (int h0 = 0; h0 < 2 * kv.Hkv; h0 += 32 / lph) {
-    const int h = h0 + lane / lph;  // k or v and head: the pages' own order
-    const bool on = h < 2 * kv.Hkv && e < kv.hd;
-    float x[8];
-    if (on) {
-      read8(src + (int64_t)h * kv.hd + e, vec, kv.hd - e, x);
-    } else {
+            const int32_t *__restrict__ start, int n_seq, int64_t n_rows, int H) {
+  __shared__ int64_t rows[RW_ROWS];
+  const int64_t i0 = blockIdx.x * (int64_t)RW_ROWS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane % LPH) * 8;
+  // k heads, then v heads: the pages' own order; RW_HEADS of them a block
+  const int first = blockIdx.y * RW_HEADS, heads = min(2 * kv.Hkv, first + RW_HEADS);
+  if (warp == 0)
+    rows[lane] = i0 + lane < n_rows ? place(kv, cu, start, n_seq, i0 + lane) : NO_SEQUENCE;
+  for (int g = warp; g < LPH; g += RW_THREADS / 32) {
+    const int r = g * (32 / LPH) + lane / LPH;
+    const bool in = i0 + r < n_rows && e < kv.hd;
+    const T *src = qkv + (i0 + r) * ld + (int64_t)H * kv.hd + e;
+    for (int h0 = first; h0 < heads; h0 += WU) {
+      float x[WU][8];
 #pragma unroll
-      for (int j = 0; j < 8; j++) x[j] = 0.f;
-    }
-    const int64_t dst = row + (int64_t)h * kv.ps;
-    if constexpr (FMT == KV_F32) {
-      if (on) write8(reinterpret_cast<float *>(kv.pages) + dst * kv.hd + e, vec, kv.hd - e, x);
-    } else if constexpr (FMT == KV_BF16) {
-      if (on)
-        write8(reinterpret_cast<__nv_bfloat16 *>(kv.pages) + dst * kv.hd + e, vec, kv.hd - e, x);
-    } else {
-      // the largest magnitude by its bits: a NaN is above an infinity
-      uint32_t top = 0;
+      for (int k = 0; k < WU; k++) {
+        if (in && h0 + k < heads) {
+          read8(src + (h0 + k) * kv.hd, VEC, kv.hd - e, x[k]);
+        } else {
 #pragma unroll
-      for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-      for (int o = 1; o < lph; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float scale = row_scale<FMT>(__uint_as_float(top));
-      const bool bad = !(__uint_as_float(top) < INFINITY);
-      const float inv = 1.f / scale;
-      const uint32_t c[2] = {bad ? 0u : encode4<FMT>(x, scale, inv),
-                             bad ? 0u : encode4<FMT>(x + 4, scale, inv)};
-      if (on) {
-        write8(kv.pages + dst * kv.hd + e, vec, kv.hd - e, c);
-        if (sub == 0) kv.scales[dst] = scale;
+          for (int j = 0; j < 8; j++) x[k][j] = 0.f;
+        }
+      }
+      if (g == warp && h0 == first) __syncthreads();  // the places are there
+      const int64_t row = rows[r];
+      const bool on = in && row >= 0;
+#pragma unroll
+      for (int k = 0; k < WU; k++) {
+        if (h0 + k >= heads) break;
+        const int64_t dst = row + (int64_t)(h0 + k) * kv.ps;
+        if constexpr (FMT == KV_F32) {
+          if (on)
+            write8(reinterpret_cast<float *>(kv.pages) + dst * kv.hd + e, VEC, kv.hd - e, x[k]);
+        } else if constexpr (FMT == KV_BF16) {
+          if (on)
+            write8(reinterpret_cast<__nv_bfloat16 *>(kv.pages) + dst * kv.hd + e, VEC, kv.hd - e,
+                   x[k]);
+        } else {
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(x[k][j]) & 0x7fffffffu);
+#pragma unroll
+          for (int o = 1; o < LPH; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          float inv;
+          const float scale = row_scale<FMT>(top, &inv);
+          uint32_t c[2] = {0u, 0u};
+          if (top < 0x7f800000u) encode8<FMT>(x[k], scale, inv, c);
+          if (on) {
+            write8(kv.pages + dst * kv.hd + e, VEC, kv.hd - e, c);
+            if (e == 0) kv.scales[dst] = scale;
+          }
+        }
       }
     }
   }
+  if (warp >= LPH) __syncthreads();  // warps without rows
 }
 
-// -------------------------------------------------------------------- read
-// One warp per packed row, as above; a row whose place does not exist reads
-// as zeros, rows of no sequence are left alone.
-template <typename T, int FMT>
+// A row without a place reads as zeros, rows of no sequence are left alone.
+template <typename T, int FMT, int LPH, bool VEC>
 __global__ void __launch_bounds__(RW_THREADS)
     k_read(const KvView kv, const int32_t *__restrict__ cu, const int32_t *__restrict__ start,
-           int n_seq, int64_t n_rows, T *__restrict__ k, T *__restrict__ v, int lph, bool vec) {
-  const int64_t i = blockIdx.x * (int64_t)(RW_THREADS / 32) + threadIdx.x / 32;
-  if (i >= n_rows) return;
-  int s;
-  const int64_t row = place(kv, cu, start, n_seq, i, &s);
-  if (s < 0) return;
-  const int lane = threadIdx.x & 31, e = (lane % lph) * 8;
+           int n_seq, int64_t n_rows, T *__restrict__ k, T *__restrict__ v) {
+  __shared__ int64_t rows[RW_ROWS];
+  const int64_t i0 = blockIdx.x * (int64_t)RW_ROWS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane % LPH) * 8;
+  const int first = blockIdx.y * RW_HEADS, heads = min(2 * kv.Hkv, first + RW_HEADS);
   const int64_t w = (int64_t)kv.Hkv * kv.hd;
-  for (int h0 = 0; h0 < 2 * kv.Hkv; h0 += 32 / lph) {
-    const int h = h0 + lane / lph;
-    if (h >= 2 * kv.Hkv || e >= kv.hd) continue;
-    float x[8] = {};
-    if (row >= 0) {
-      const int64_t src = row + (int64_t)h * kv.ps;
-      kv_read8<FMT>(kv.pages, src * kv.hd + e, vec, kv.hd - e, x);
-      if constexpr (FMT >= KV_E4M3) {
-        const float sc = kv.scales[src];
+  if (warp == 0)
+    rows[lane] = i0 + lane < n_rows ? place(kv, cu, start, n_seq, i0 + lane) : NO_SEQUENCE;
+  __syncthreads();
+  for (int g = warp; g < LPH; g += RW_THREADS / 32) {
+    const int r = g * (32 / LPH) + lane / LPH;
+    const int64_t row = rows[r];
+    if (row == NO_SEQUENCE || e >= kv.hd) continue;
+    T *kd = k + (i0 + r) * w + e, *vd = v + (i0 + r) * w - w + e;  // v of head h - Hkv
+    for (int h0 = first; h0 < heads; h0 += RU) {
+      float x[RU][8], sc[RU];
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[j] *= sc;
+      for (int m = 0; m < RU; m++) {
+        sc[m] = 1.f;
+        if (row >= 0 && h0 + m < heads) {
+          const int64_t src = row + (int64_t)(h0 + m) * kv.ps;
+          kv_read8<FMT>(kv.pages, src * kv.hd + e, VEC, kv.hd - e, x[m]);
+          if constexpr (FMT >= KV_E4M3) sc[m] = kv.scales[src];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; j++) x[m][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < RU; m++) {
+        const int h = h0 + m;
+        if (h >= heads) break;
+        if constexpr (FMT >= KV_E4M3) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) x[m][j] *= sc[m];
+        }
+        write8((h < kv.Hkv ? kd : vd) + (int64_t)h * kv.hd, VEC, kv.hd - e, x[m]);
       }
     }
-    T *dst = h < kv.Hkv ? k + i * w + (int64_t)h * kv.hd
-                        : v + i * w + (int64_t)(h - kv.Hkv) * kv.hd;
-    write8(dst + e, vec, kv.hd - e, x);
   }
 }
 
@@ -1193,41 +1245,61 @@ static int64_t pre_bytes(int n_seq) { return (4 * ((int64_t)n_seq + 1) + 255) / 
 
 }  // namespace pg
 
+namespace pg {
+static dim3 rw_grid(const KvView &kv, int64_t n_rows) {
+  return dim3(cdiv(n_rows, RW_ROWS), cdiv(2 * kv.Hkv, RW_HEADS));
+}
+// Calls f with the element type, cache format, lanes of a head and vector
+// access as constants.
+template <typename F>
+static void rw_dispatch(DType dt, int fmt, int hd, bool vec, F f) {
+  auto with = [&](auto t, auto m, auto l) {
+    vec ? f(t, m, l, std::true_type()) : f(t, m, l, std::false_type());
+  };
+  auto lanes = [&](auto t, auto m) {
+    if (hd <= 8) with(t, m, std::integral_constant<int, 1>());
+    else if (hd <= 16) with(t, m, std::integral_constant<int, 2>());
+    else if (hd <= 32) with(t, m, std::integral_constant<int, 4>());
+    else if (hd <= 64) with(t, m, std::integral_constant<int, 8>());
+    else with(t, m, std::integral_constant<int, 16>());
+  };
+  auto format = [&](auto t) {
+    switch (fmt) {
+      case KV_F32: lanes(t, std::integral_constant<int, KV_F32>()); break;
+      case KV_BF16: lanes(t, std::integral_constant<int, KV_BF16>()); break;
+      case KV_E4M3: lanes(t, std::integral_constant<int, KV_E4M3>()); break;
+      default: lanes(t, std::integral_constant<int, KV_INT8>());
+    }
+  };
+  if (dt == DT_BF16) format(__nv_bfloat16());
+  else format(float());
+}
+}  // namespace pg
+
 void kv_write(const KvView &kv, const void *qkv, int64_t ld, DType dt, const int32_t *cu,
               const int32_t *start, int n_seq, int64_t n_rows, int H, cudaStream_t s) {
   using namespace pg;
-  int lph = 1;  // lanes of a head
-  while (lph * 8 < kv.hd) lph *= 2;
   const bool vec = kv.hd % 8 == 0 && ld % 8 == 0 && !((uintptr_t)qkv & 15) &&
                    !((uintptr_t)kv.pages & 15);
-  const unsigned grid = cdiv(n_rows, RW_THREADS / 32);
-#define GO(T, F)                                                                                 \
-  k_write<T, F><<<grid, RW_THREADS, 0, s>>>(kv, (const T *)qkv, ld, cu, start, n_seq, n_rows, H, \
-                                            lph, vec)
-#define FMT(T)                                                                                 \
-  switch (kv.fmt) {                                                                            \
-    case KV_F32: GO(T, KV_F32); break;                                                         \
-    case KV_BF16: GO(T, KV_BF16); break;                                                       \
-    case KV_E4M3: GO(T, KV_E4M3); break;                                                       \
-    default: GO(T, KV_INT8);                                                                   \
-  }
-  if (dt == DT_BF16) { FMT(__nv_bfloat16) } else { FMT(float) }
-#undef GO
+  rw_dispatch(dt, kv.fmt, kv.hd, vec, [&](auto t, auto m, auto l, auto v) {
+    using T = decltype(t);
+    k_write<T, decltype(m)::value, decltype(l)::value, decltype(v)::value>
+        <<<rw_grid(kv, n_rows), RW_THREADS, 0, s>>>(kv, (const T *)qkv, ld, cu, start, n_seq,
+                                                      n_rows, H);
+  });
   count_launch();
 }
 
 void kv_read(const KvView &kv, const int32_t *cu, const int32_t *start, int n_seq, int64_t n_rows,
              void *k, void *v, DType dt, cudaStream_t s) {
   using namespace pg;
-  int lph = 1;
-  while (lph * 8 < kv.hd) lph *= 2;
   const bool vec = kv.hd % 8 == 0 && !(((uintptr_t)k | (uintptr_t)v | (uintptr_t)kv.pages) & 15);
-  const unsigned grid = cdiv(n_rows, RW_THREADS / 32);
-#define GO(T, F)                                                                                \
-  k_read<T, F><<<grid, RW_THREADS, 0, s>>>(kv, cu, start, n_seq, n_rows, (T *)k, (T *)v, lph, vec)
-  if (dt == DT_BF16) { FMT(__nv_bfloat16) } else { FMT(float) }
-#undef GO
-#undef FMT
+  rw_dispatch(dt, kv.fmt, kv.hd, vec, [&](auto t, auto m, auto l, auto x) {
+    using T = decltype(t);
+    k_read<T, decltype(m)::value, decltype(l)::value, decltype(x)::value>
+        <<<rw_grid(kv, n_rows), RW_THREADS, 0, s>>>(kv, cu, start, n_seq, n_rows, (T *)k,
+                                                      (T *)v);
+  });
   count_launch();
 }
 

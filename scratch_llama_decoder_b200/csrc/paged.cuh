@@ -23,12 +23,12 @@ inline int kv_bytes(int fmt) { return fmt == KV_F32 ? 4 : fmt == KV_BF16 ? 2 : 1
 // kv head 0's keys; -1 when the table does not hold the position or names a
 // page that does not exist.
 LLM_DEV int64_t kv_row(const KvView &kv, int s, int64_t pos) {
-  if (pos < 0) return -1;
-  const int64_t pg = pos / kv.ps;
-  if (pg >= kv.table_pages) return -1;
+  // table_pages * ps is at most 2^30: 32-bit division from here on
+  if (pos < 0 || pos >= (int64_t)kv.table_pages * kv.ps) return -1;
+  const uint32_t pg = (uint32_t)pos / (uint32_t)kv.ps;
   const int64_t page = kv.table[(int64_t)s * kv.table_ld + pg];
   if (page < 0 || page >= kv.n_pages) return -1;
-  return page * (2 * (int64_t)kv.Hkv * kv.ps) + pos % kv.ps;
+  return page * (2 * (int64_t)kv.Hkv * kv.ps) + ((uint32_t)pos - pg * (uint32_t)kv.ps);
 }
 
 void kv_write(const KvView &kv, const void *qkv, int64_t ld, DType dt, const int32_t *cu,
