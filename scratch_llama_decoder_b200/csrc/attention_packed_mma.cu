@@ -136,10 +136,12 @@ __global__ void __launch_bounds__(NT)
   }
   float L2[2], Dr[2];
 #pragma unroll
-  for (int r = 0; r < 2; r++) {  // D from dO's fragments and O read the same way
+  for (int r = 0; r < 2; r++) {
     const int q = 16 * w + (lane >> 2) + 8 * r;
-    float part = 0.f;
-    if (q < nq) {
+    // rows past the sequence: P = 0
+    L2[r] = q < nq ? lse[(int64_t)h * n_rows + t.row0 + q0 + q] * LOG2E : INFINITY;
+    Dr[r] = 0.f;
+    if (q0 > 0 && q < nq) {  // D from dO's fragments and O read the same way
       const bf16 *orow = o + orow0 + q * ow;
 #pragma unroll
       for (int k = 0; k < HD / 16; k++)
@@ -150,16 +152,53 @@ __global__ void __launch_bounds__(NT)
             const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(orow + c));
             const float2 b =
                 __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&df[k][2 * e + r]));
-            part += a.x * b.x + a.y * b.y;
+            Dr[r] += a.x * b.x + a.y * b.y;
           }
         }
     }
-    part += __shfl_xor_sync(0xffffffffu, part, 1);
-    part += __shfl_xor_sync(0xffffffffu, part, 2);
-    Dr[r] = part;
-    const int64_t li = (int64_t)h * n_rows + t.row0 + q0 + q;
-    L2[r] = q < nq ? lse[li] * LOG2E : INFINITY;  // rows past the sequence: P = 0
-    if ((lane & 3) == 0 && q < nq) D[li] = part;
+  }
+  if (q0 == 0) {
+    // a sequence's first 64 rows: D = sum_j P_ij dP_ij / sum_j P_ij of their one
+    // tile (the quotient, so that P's own errors cancel where dP is the same for
+    // all).  dO . O takes O as it was rounded to bf16, and where O has few terms
+    // that error is as large as dS's own.
+    float l[2] = {0.f, 0.f};
+    wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int hf = 0; hf < 2; hf++) {
+      float s[4][4] = {}, dp[4][4] = {};
+#pragma unroll
+      for (int k = 0; k < HD / 16; k++) {
+        abt_step(s, qf[k], Ks, 32 * hf, k);
+        abt_step(dp, df[k], Vs, 32 * hf, k);
+      }
+#pragma unroll
+      for (int nt = 0; nt < 4; nt++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int r = e >> 1, q = 16 * w + (lane >> 2) + 8 * r;
+          const int key = 32 * hf + 8 * nt + (lane & 3) * 2 + (e & 1);
+          if (key <= q) {
+            const float p = tc::ex2(s[nt][e] * sl2 - L2[r]);
+            Dr[r] += p * dp[nt][e];
+            l[r] += p;
+          }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      Dr[r] = l[r] > 0.f ? Dr[r] / l[r] : 0.f;  // 0: a row past the sequence
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; r++) {
+    Dr[r] += __shfl_xor_sync(0xffffffffu, Dr[r], 1);
+    Dr[r] += __shfl_xor_sync(0xffffffffu, Dr[r], 2);
+    const int q = 16 * w + (lane >> 2) + 8 * r;
+    if ((lane & 3) == 0 && q < nq) D[(int64_t)h * n_rows + t.row0 + q0 + q] = Dr[r];
   }
   float acc[HD / 8][4];
 #pragma unroll

@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float sl2 = scale * LOG2E;
     bool ok = true;
     int gb = 0, st_slot = -1;  // slot whose dQ store is still to be released
+    int qr = 0;  // uses of the row groups' exchange (red, qred)
     for (int rr = 0, it = 0; ok; rr++, it++) {
       const int item = sched_item(rr, G, cta);
       if (item >= n_items) break;
@@ -430,17 +431,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float nl2 = valid ? -sNL[r] * LOG2E : -INFINITY;
       mbar_arrive(o_empty);              // this thread's O row and -L consumed
       mbar_arrive(qd_empty + 8 * slot);  // and its dO row
-      float *rd = red + (it & 1) * NCQ * 128;
-      rd[cq * 128 + r] = dpart;
-      // the row's four column groups are the four warps of this lane quarter
-      mbar_arrive(qred + 8 * quarter);
-      if (!warp_wait(qred + 8 * quarter, it & 1, abort_sh, gflag)) {
+      // sum of v over the row's four column groups, the four warps of this lane
+      // quarter (false: a wait gave up)
+      auto row_sum = [&](float v, float &sum) {
+        float *rd = red + (qr & 1) * NCQ * 128;
+        rd[cq * 128 + r] = v;
+        mbar_arrive(qred + 8 * quarter);
+        if (!warp_wait(qred + 8 * quarter, qr & 1, abort_sh, gflag)) return false;
+        qr++;
+        sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < NCQ; c++) sum += rd[c * 128 + r];
+        return true;
+      };
+      // Packed, a sequence's first 128 rows: D = sum_j P_ij dP_ij / sum_j P_ij of
+      // their one block instead (below; the quotient, so that P's own errors
+      // cancel where dP is the same for all).  dO . O takes O as it was rounded
+      // to bf16, and where O has few terms that error is as large as dS's own.
+      const bool own_d = PK && nj == 1;
+      float Di = 0.f;
+      if (!own_d && !row_sum(dpart, Di)) {
         ok = false;
         break;
       }
-      float Di = 0.f;
-#pragma unroll
-      for (int c = 0; c < NCQ; c++) Di += rd[c * 128 + r];
       // the previous item's dQ store has long read its tile: release the slot
       if (st_slot >= 0) {
         if (lane == 0) {
@@ -449,8 +462,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         st_slot = -1;
       }
-      if (cq == 0 && valid) Dv[stat(im, h) + qi] = Di;
-      const float2 nl = make_float2(nl2, nl2), nd = make_float2(-Di, -Di);
+      if (!own_d && cq == 0 && valid) Dv[stat(im, h) + qi] = Di;
+      const float2 nl = make_float2(nl2, nl2);
+      float2 nd = make_float2(-Di, -Di);
       for (int j = 0; j < nj && ok; j++, gb++) {
         if (!warp_wait(s_full, gb & 1, abort_sh, gflag)) {
           ok = false;
@@ -466,6 +480,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int k0 = j * BK + cq * CW;
         const bool diag = (j == qb);  // only the diagonal block masks (keys >= T lie above it)
         uint32_t w[CW / 2];
+        if (PK && own_d) {
+          float part = 0.f, l = 0.f;
+#pragma unroll
+          for (int i = 0; i < CW; i += 2) {
+            const float2 p = exp2_split<NP_DQ>(
+                __ffma2_rn(make_float2(sv[i], sv[i + 1]), make_float2(sl2, sl2), nl), i / 2);
+            if (k0 + i <= qi) {
+              part += p.x * dv[i];
+              l += p.x;
+            }
+            if (k0 + i + 1 <= qi) {
+              part += p.y * dv[i + 1];
+              l += p.y;
+            }
+          }
+          if (!row_sum(part, Di) || !row_sum(l, part)) {
+            ok = false;
+            break;
+          }
+          Di /= part;
+          if (cq == 0 && valid) Dv[stat(im, h) + qi] = Di;
+          nd = make_float2(-Di, -Di);
+        }
         if (diag) {  // the causal mask only on the diagonal block
 #pragma unroll
           for (int i = 0; i < CW; i += 2) {

@@ -583,8 +583,11 @@ __global__ void __launch_bounds__(AT)
 // be left to the products' end, so it joins the weight: 2^(s + log2 scale -
 // mo), whose reference mo of its own (the running maximum of s + log2 scale)
 // holds it within float16 whatever the scales are.
-// The bfloat16 and float16 rounding of the weights (2^-9 and 2^-12) is the
-// only rounding below 32 bits; the sum l takes them unrounded.
+// The rounding of the weights to float16 (2^-12) is the only one below 32
+// bits, and the sum l takes them unrounded; a bfloat16 cache takes each weight
+// as two bfloat16 terms (2^-17: rounded to one, the outputs of a long context
+// were 1.45 times as far off as their own rounding; the loads hide the second
+// product).
 constexpr int NW = AT / 32;
 // Blocks per SM: what the registers of a lane's operands leave room for.
 constexpr int mma_blocks(int HD, int NT) { return NT == 2 ? 2 : HD == 128 ? 3 : 4; }
@@ -1006,7 +1009,7 @@ __global__ void __launch_bounds__(AT, mma_blocks(HD, NT))
             }
         }
         // weights and their B fragments
-        uint32_t pf[NT][SB][2];
+        uint32_t pf[NT][SB][2], pl[NT][SB][2];  // pl: what pf's rounding left (bfloat16)
 #pragma unroll
         for (int n = 0; n < NT; n++) {
           float ref[GC], refo[GC];
@@ -1026,7 +1029,11 @@ __global__ void __launch_bounds__(AT, mma_blocks(HD, NT))
                 l[n][c] += p[c];
                 if constexpr (!BF) p[c] = ex2(x[n][b][hf][c] + (lv[b][hf] - refo[c]));
               }
-              pf[n][b][hf] = transpose8(pack16<BF>(p[0], p[1]));
+              const uint32_t w = pack16<BF>(p[0], p[1]);
+              pf[n][b][hf] = transpose8(w);
+              if constexpr (BF)
+                pl[n][b][hf] = transpose8(pack16<BF>(p[0] - __uint_as_float(w << 16),
+                                                     p[1] - __uint_as_float(w & 0xffff0000u)));
             }
         }
         // O^T += V^T P^T: tile i holds columns d and d + 1 of word i (bf16), or
@@ -1041,8 +1048,10 @@ __global__ void __launch_bounds__(AT, mma_blocks(HD, NT))
               const uint32_t a2 = __byte_perm(vr[b][2][i], vr[b][3][i], 0x5410);
               const uint32_t a3 = __byte_perm(vr[b][2][i], vr[b][3][i], 0x7632);
 #pragma unroll
-              for (int n = 0; n < NT; n++)
+              for (int n = 0; n < NT; n++) {
                 mma<BF>(acc[n][i], a0, a1, a2, a3, pf[n][b][0], pf[n][b][1]);
+                mma<BF>(acc[n][i], a0, a1, a2, a3, pl[n][b][0], pl[n][b][1]);
+              }
             } else {
               uint32_t u[4], w[4];  // columns 0 .. 3 of the word: keys 2t, 2t+1; 2t+8, 2t+9
               half_pairs<FMT>(__byte_perm(vr[b][0][i], vr[b][1][i], 0x5140), u[0], u[1]);

@@ -62,7 +62,10 @@ def _one(q, k, v):
 
 
 def backward(qkv, cu, h, g, out, lse, dout, want):
-    """dqkv and its error bound, from the formulas on the given out and lse."""
+    """dqkv and its error bound, from the formulas with the given lse; D is the
+    exact sum_j P_ij dP_ij.  A kernel may take it as dout . out instead: out is
+    off by its own bound (attention's), D by that times |dout|, summed.  Or it
+    may form the sum from its own weights: off by their errors times |dP - D|."""
     n, hd = qkv.shape[0], qkv.shape[1] // (h + 2 * g)
     c = 1 / math.sqrt(hd)
     q, k, v = split(qkv, h, g)
@@ -81,13 +84,16 @@ def backward(qkv, cu, h, g, out, lse, dout, want):
             L = lse[i, a:b].double()[:, None]
             s = Q @ K.t() * c
             p = torch.exp(torch.where(keep > 0, s - L, torch.full_like(s, -math.inf)))
-            D = (G * O).sum(1, keepdim=True)
             dP = G @ V.t()
+            D = (p * dP).sum(1, keepdim=True)
             ds = p * (dP - D)
             # weight error (its score, L and their difference), then dS's
             ep = ((hd + 3) * U * (Q.abs() @ K.abs().t()) * c + 3 * U * (s.abs() + L.abs()) + ex) * p
+            rel = 2 * (ep.sum(1, keepdim=True) + ex) + (2 * m + 16) * U + r
+            eo = rel * (p @ V.abs()) + R[want] * O.abs()  # out's bound
+            eD = (G.abs() * eo).sum(1, keepdim=True) + (ep * (dP - D).abs()).sum(1, keepdim=True)
             eds = (p * (hd + 2) * U * (G.abs() @ V.abs().t() + (G * O).abs().sum(1, keepdim=True))
-                   + ep * (dP - D).abs() + (r + 3 * U) * ds.abs())
+                   + p * eD + ep * (dP - D).abs() + (r + 3 * U) * ds.abs())
             sums = (m * (h // g) + 8) * U
             dx[a:b, i] = ds @ K * c
             bd[a:b, i] = (eds + sums * ds.abs()) @ K.abs() * c
