@@ -31,6 +31,8 @@ assert _KV.size == C.sizeof(L.llm_kv)
 # The current stream's handle as an integer: torch.cuda.current_stream() builds
 # a Stream object for it (2 us of a call whose kernel takes 5).
 _stream = torch._C._cuda_getCurrentRawStream
+_current = torch.cuda.current_device
+_empty = torch.empty
 _packed_fwd = L.lib.llm_kernel_attention_packed_fwd
 _packed_bwd = L.lib.llm_kernel_attention_packed_bwd
 _write, _read = L.lib.llm_kernel_kv_write, L.lib.llm_kernel_kv_read
@@ -41,55 +43,57 @@ def _bad(what):
     raise ValueError(what)
 
 
-def _on(dev, fn, *args):
-    """fn(*args, stream) with the tensors' device current."""
-    i = dev.index
-    if i == torch.cuda.current_device():
+def _on(i, fn, *args):
+    """fn(*args, stream) with the tensors' device (index i) current."""
+    if i == _current():
         rc = fn(*args, _stream(i))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(i):
             rc = fn(*args, _stream(i))
     if rc:
         L.check(rc, fn.__name__)
 
 
 def _rows(name, t):
-    """dtype code and row stride of a 2-D float32/bfloat16 tensor of rows, which
-    may be spaced (stride(1) == 1)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2 or t.dtype not in _DTYPES:
+    """dtype code, device index and row stride of a 2-D float32/bfloat16 tensor
+    of rows, which may be spaced (stride(1) == 1)."""
+    dt = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) and t.dim() == 2 else None
+    i = t.get_device() if dt is not None else -1
+    if i < 0:
         _bad(f"{name} must be a 2-D float32 or bfloat16 tensor on a CUDA device")
-    n, w = t.shape
     ld, step = t.stride()
+    w = t.shape[1]
     if step != 1 and w != 1:
         _bad(f"{name}: the elements of a row must be adjacent")
     if ld < w:
-        if n > 1:
+        if t.shape[0] > 1:
             _bad(f"{name}: its rows overlap")
         ld = w
-    return _DTYPES[t.dtype], ld
+    return dt, i, ld
 
 
-def _at(name, t, dev, shape, dtype):
+def _at(name, t, i, shape, dtype):
     """Address of a contiguous tensor of this device, shape and type."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dtype or \
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != i or \
             t.shape != shape or not t.is_contiguous():
-        _bad(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+        _bad(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{i}")
     return t.data_ptr()
 
 
-def _flag(t, dev):
+def _flag(t, i):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != _i32 or t.numel() != 1:
-        _bad(f"flag must be one int32 element on {dev}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != i or t.dtype is not _i32 or \
+            t.numel() != 1:
+        _bad(f"flag must be one int32 element on cuda:{i}")
     return t.data_ptr()
 
 
-def _offsets(t, dev):
+def _offsets(t, i):
     """Address of cu_seqlens and the number of sequences."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != _i32 or t.dim() != 1 or \
-            t.shape[0] < 1 or not t.is_contiguous():
-        _bad(f"cu_seqlens must be a contiguous 1-D int32 tensor on {dev}, one offset more than "
+    if not isinstance(t, torch.Tensor) or t.dtype is not _i32 or t.get_device() != i or \
+            t.dim() != 1 or not t.is_contiguous() or t.shape[0] < 1:
+        _bad(f"cu_seqlens must be a contiguous 1-D int32 tensor on cuda:{i}, one offset more than "
              "there are sequences")
     return t.data_ptr(), t.shape[0] - 1
 
@@ -121,24 +125,24 @@ def attention_packed(qkv, cu_seqlens, n_head, n_kv_head, out=None, lse=None, fla
     cu_seqlens[s + 1] - 1.  Returns (out [rows, n_head * head_dim] in qkv's
     type, lse float32 [n_head, rows]); rows of no sequence keep what out and
     lse held (nothing useful unless they are given)."""
-    dt, ld = _rows("qkv", qkv)
+    dt, i, ld = _rows("qkv", qkv)
     n_rows, width = qkv.shape
     hd, dev = _head_dim(width, n_head, n_kv_head), qkv.device
-    cu, n_seq = _offsets(cu_seqlens, dev)
+    cu, n_seq = _offsets(cu_seqlens, i)
     nb = _packed_bytes(n_rows, n_seq, n_head, 0)
     if out is None:
-        out = torch.empty((n_rows, n_head * hd), dtype=qkv.dtype, device=dev)
+        out = _empty((n_rows, n_head * hd), dtype=qkv.dtype, device=dev)
         o = out.data_ptr()
     else:
-        o = _at("out", out, dev, (n_rows, n_head * hd), qkv.dtype)
+        o = _at("out", out, i, (n_rows, n_head * hd), qkv.dtype)
     if lse is None:
-        lse = torch.empty((n_head, n_rows), dtype=_f32, device=dev)
+        lse = _empty((n_head, n_rows), dtype=_f32, device=dev)
         ls = lse.data_ptr()
     else:
-        ls = _at("lse", lse, dev, (n_head, n_rows), _f32)
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-    _on(dev, _packed_fwd, qkv.data_ptr(), ld, dt, cu, n_seq, n_rows, n_head, n_kv_head, hd, o, ls,
-        ws.data_ptr(), nb, _flag(flag, dev))
+        ls = _at("lse", lse, i, (n_head, n_rows), _f32)
+    ws = _empty(nb, dtype=torch.uint8, device=dev)
+    _on(i, _packed_fwd, qkv.data_ptr(), ld, dt, cu, n_seq, n_rows, n_head, n_kv_head, hd, o, ls,
+        ws.data_ptr(), nb, _flag(flag, i))
     return out, lse
 
 
@@ -148,24 +152,24 @@ def attention_packed_backward(qkv, cu_seqlens, n_head, n_kv_head, out, lse, dout
     inputs, its out and lse, and the gradient dout of out, the gradient of qkv
     (rows of no sequence keep what dqkv held: nothing useful unless it is
     given; its rows may be spaced)."""
-    dt, ld = _rows("qkv", qkv)
+    dt, i, ld = _rows("qkv", qkv)
     n_rows, width = qkv.shape
     hd, dev = _head_dim(width, n_head, n_kv_head), qkv.device
-    cu, n_seq = _offsets(cu_seqlens, dev)
+    cu, n_seq = _offsets(cu_seqlens, i)
     nb = _packed_bytes(n_rows, n_seq, n_head, 1)
-    o = _at("out", out, dev, (n_rows, n_head * hd), qkv.dtype)
-    ls = _at("lse", lse, dev, (n_head, n_rows), _f32)
-    do = _at("dout", dout, dev, (n_rows, n_head * hd), qkv.dtype)
+    o = _at("out", out, i, (n_rows, n_head * hd), qkv.dtype)
+    ls = _at("lse", lse, i, (n_head, n_rows), _f32)
+    do = _at("dout", dout, i, (n_rows, n_head * hd), qkv.dtype)
     if dqkv is None:
-        dqkv = torch.empty((n_rows, width), dtype=qkv.dtype, device=dev)
+        dqkv = _empty((n_rows, width), dtype=qkv.dtype, device=dev)
         dld = width
     else:
-        ddt, dld = _rows("dqkv", dqkv)
-        if ddt != dt or dqkv.device != dev or dqkv.shape != qkv.shape:
-            _bad(f"dqkv must be of qkv's type and shape, on {dev}")
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-    _on(dev, _packed_bwd, qkv.data_ptr(), ld, dt, cu, n_seq, n_rows, n_head, n_kv_head, hd, o, ls,
-        do, dqkv.data_ptr(), dld, ws.data_ptr(), nb, _flag(flag, dev))
+        ddt, di, dld = _rows("dqkv", dqkv)
+        if ddt != dt or di != i or dqkv.shape != qkv.shape:
+            _bad(f"dqkv must be of qkv's type and shape, on cuda:{i}")
+    ws = _empty(nb, dtype=torch.uint8, device=dev)
+    _on(i, _packed_bwd, qkv.data_ptr(), ld, dt, cu, n_seq, n_rows, n_head, n_kv_head, hd, o, ls,
+        do, dqkv.data_ptr(), dld, ws.data_ptr(), nb, _flag(flag, i))
     return dqkv
 
 
@@ -183,31 +187,32 @@ def kv_pages(n_pages, page_size, n_kv_head, head_dim, format="bf16", device="cud
 
 
 def _kv(pages, scales, table, flag):
-    """The cache's packed llm_kv, its device, kv heads and head size."""
-    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dim() != 5 or \
-            pages.shape[1] != 2 or pages.dtype not in _FORMATS or not pages.is_contiguous():
+    """The cache's packed llm_kv, its device index and shape."""
+    fmt = _FORMATS.get(pages.dtype) if isinstance(pages, torch.Tensor) and pages.dim() == 5 else None
+    i = pages.get_device() if fmt is not None else -1
+    shape = pages.shape if i >= 0 else (0, 0)
+    if shape[1] != 2 or not pages.is_contiguous():
         _bad("pages must be a contiguous [n_pages, 2, n_kv_head, page_size, head_dim] tensor on a "
              "CUDA device, of float32, bfloat16, float8_e4m3fn or int8")
-    fmt, dev, shape = _FORMATS[pages.dtype], pages.device, pages.shape
+    n, _, g, ps, hd = shape
     sc = 0
     if fmt >= L.LLM_KV_E4M3:
         if scales is None:
             _bad("an 8-bit cache needs its scales")
-        sc = _at("scales", scales, dev, shape[:4], _f32)
-    if not isinstance(table, torch.Tensor) or table.device != dev or table.dtype != _i32 or \
-            table.dim() != 2:
-        _bad(f"table must be a 2-D int32 tensor on {dev}")
-    cols = table.shape[1]
+        sc = _at("scales", scales, i, (n, 2, g, ps), _f32)
+    if not isinstance(table, torch.Tensor) or table.dtype is not _i32 or \
+            table.get_device() != i or table.dim() != 2:
+        _bad(f"table must be a 2-D int32 tensor on cuda:{i}")
     ld, step = table.stride()
+    cols = table.shape[1]
     if step != 1 and cols > 1:
         _bad("table: the entries of a row must be adjacent")
     if ld < cols:
         if table.shape[0] > 1:
             _bad("table: its rows overlap")
         ld = cols
-    n, _, g, ps, hd = shape
     return _KV.pack(pages.data_ptr(), sc, table.data_ptr(), ld, n, cols, fmt, g, hd, ps,
-                    _flag(flag, dev) or 0), dev, g, hd
+                    0 if flag is None else _flag(flag, i)), i, g, hd, ps, cols
 
 
 def kv_write(qkv, cu_seqlens, n_head, pages, table, scales=None, starts=None, flag=None):
@@ -216,16 +221,16 @@ def kv_write(qkv, cu_seqlens, n_head, pages, table, scales=None, starts=None, fl
 
     qkv, cu_seqlens: as in attention_packed; pages, scales: of kv_pages; table:
     int32 [n_seq, pages a sequence]; starts: int32 [n_seq] (None: all 0)."""
-    dt, ld = _rows("qkv", qkv)
-    kv, dev, g, hd = _kv(pages, scales, table, flag)
+    dt, qi, ld = _rows("qkv", qkv)
+    kv, i, g, hd, _, _ = _kv(pages, scales, table, flag)
     n_rows, width = qkv.shape
-    if qkv.device != dev or width != (n_head + 2 * g) * hd:
-        _bad(f"qkv must have (n_head + 2 n_kv_head) * head_dim columns, on {dev}")
-    cu, n_seq = _offsets(cu_seqlens, dev)
+    if qi != i or width != (n_head + 2 * g) * hd:
+        _bad(f"qkv must have (n_head + 2 n_kv_head) * head_dim columns, on cuda:{i}")
+    cu, n_seq = _offsets(cu_seqlens, i)
     if table.shape[0] < n_seq:
         _bad("table must have a row for every sequence")
-    st = None if starts is None else _at("starts", starts, dev, (n_seq,), _i32)
-    _on(dev, _write, kv, qkv.data_ptr(), ld, dt, cu, st, n_seq, n_rows, n_head)
+    st = None if starts is None else _at("starts", starts, i, (n_seq,), _i32)
+    _on(i, _write, kv, qkv.data_ptr(), ld, dt, cu, st, n_seq, n_rows, n_head)
 
 
 def kv_read(pages, table, cu_seqlens, n_rows, dtype, scales=None, starts=None, k=None, v=None,
@@ -233,20 +238,26 @@ def kv_read(pages, table, cu_seqlens, n_rows, dtype, scales=None, starts=None, k
     """The inverse of kv_write (llm_kernel_kv_read): (k, v), each [n_rows,
     n_kv_head, head_dim] of dtype (float32 or bfloat16); rows of no sequence
     keep what k and v held (nothing useful unless they are given)."""
-    if dtype not in _DTYPES:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         _bad("dtype must be torch.float32 or torch.bfloat16")
-    kv, dev, g, hd = _kv(pages, scales, table, flag)
-    cu, n_seq = _offsets(cu_seqlens, dev)
+    kv, i, g, hd, _, _ = _kv(pages, scales, table, flag)
+    cu, n_seq = _offsets(cu_seqlens, i)
     if table.shape[0] < n_seq:
         _bad("table must have a row for every sequence")
-    shape = (n_rows, g, hd)
-    st = None if starts is None else _at("starts", starts, dev, (n_seq,), _i32)
+    shape, dev = (n_rows, g, hd), pages.device
+    st = None if starts is None else _at("starts", starts, i, (n_seq,), _i32)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=dev)
+        k = _empty(shape, dtype=dtype, device=dev)
+        kp = k.data_ptr()
+    else:
+        kp = _at("k", k, i, shape, dtype)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=dev)
-    _on(dev, _read, kv, cu, st, n_seq, n_rows, _at("k", k, dev, shape, dtype),
-        _at("v", v, dev, shape, dtype), _DTYPES[dtype])
+        v = _empty(shape, dtype=dtype, device=dev)
+        vp = v.data_ptr()
+    else:
+        vp = _at("v", v, i, shape, dtype)
+    _on(i, _read, kv, cu, st, n_seq, n_rows, kp, vp, dt)
     return k, v
 
 
@@ -270,28 +281,29 @@ def attention_paged(q, pages, table, lens, scales=None, out=None, lse=None, flag
     kv_write; lens: int32 [n_seq].  Returns (out [n_seq, n_head * head_dim] in
     q's type, lse float32 [n_seq, n_head]); a sequence of length 0 gets out 0
     and lse -inf."""
-    kv, dev, g, hd = _kv(pages, scales, table, flag)
-    dt, ld = _rows("q", q)
+    kv, i, g, hd, ps, cols = _kv(pages, scales, table, flag)
+    dt, qi, ld = _rows("q", q)
     n_seq, width = q.shape
     n_head = width // hd if hd else 0
-    if q.device != dev or not hd or width % hd or not g or n_head % g:
-        _bad(f"q must have n_head * head_dim columns, n_head a multiple of n_kv_head, on {dev}")
+    if qi != i or not hd or width % hd or not g or n_head % g:
+        _bad(f"q must have n_head * head_dim columns, n_head a multiple of n_kv_head, on cuda:{i}")
     if table.shape[0] < n_seq:
         _bad("table must have a row for every sequence")
-    ln = _at("lens", lens, dev, (n_seq,), _i32)
-    nb = _paged_bytes(g, hd, pages.shape[3], table.shape[1], n_seq, n_head)
+    ln = _at("lens", lens, i, (n_seq,), _i32)
+    nb = _paged_bytes(g, hd, ps, cols, n_seq, n_head)
+    dev = q.device
     if out is None:
-        out = torch.empty((n_seq, width), dtype=q.dtype, device=dev)
+        out = _empty((n_seq, width), dtype=q.dtype, device=dev)
         o = out.data_ptr()
     else:
-        o = _at("out", out, dev, (n_seq, width), q.dtype)
+        o = _at("out", out, i, (n_seq, width), q.dtype)
     if lse is None:
-        lse = torch.empty((n_seq, n_head), dtype=_f32, device=dev)
+        lse = _empty((n_seq, n_head), dtype=_f32, device=dev)
         ls = lse.data_ptr()
     else:
-        ls = _at("lse", lse, dev, (n_seq, n_head), _f32)
+        ls = _at("lse", lse, i, (n_seq, n_head), _f32)
     # a call that splits nothing needs no workspace
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    _on(dev, _paged, kv, q.data_ptr(), ld, dt, ln, n_seq, n_head, o, ls,
+    ws = _empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    _on(i, _paged, kv, q.data_ptr(), ld, dt, ln, n_seq, n_head, o, ls,
         ws.data_ptr() if nb else None, nb)
     return out, lse
