@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
   for (int s = threadIdx.x >> 5; s < n_seq; s += PT / 32) {
     const int row0 = off[s], len = off[s + 1] - row0, n = (len + block - 1) / block;
     for (int b = threadIdx.x & 31; b < n; b += 32)
-      tiles[hist[b + 1] + rank[s]] = PkTile{row0, len, b, 0};
+      tiles[hist[b + 1] + rank[s]] = PkTile{row0, len, b, s};
   }
 }
 
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
   }
   for (int s = t >> 5; s < n_seq; s += FEW / 32)
     for (int b = t & 31; b < blocks[s]; b += 32)
-      tiles[base[b + 1] + rank[s]] = PkTile{off[s], off[s + 1] - off[s], b, 0};
+      tiles[base[b + 1] + rank[s]] = PkTile{off[s], off[s + 1] - off[s], b, s};
 }
 
 // --------------------------------------------------------- CUDA-core kernels

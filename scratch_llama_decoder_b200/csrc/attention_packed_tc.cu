@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // ------------------------------------------------------ TMA producer
       int gb = 0, nq[2] = {0, 0};  // key blocks, Q tiles of each stream issued
       bool ok = true;
-      const int n_items = pk.tiles ? ld_int(pk.n_tiles) * heads : only.w * gridDim.x;
+      const int n_items = pk.tiles ? ld_int(pk.n_tiles) * heads : only.w ? gridDim.x : 0;
       int item = blockIdx.x;
       for (int it = 0;; it++) {
         int4 t = make_int4(-1, 0, 0, 0);
@@ -541,7 +541,7 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
   // the plan's kernel, 8.9 without)
   const bool plan = items > device_sms() || a.n_seq > PK_FIND_SEQ;
   const PkView pk{p.n_tiles, plan ? p.tiles : nullptr, a.n_rows, (__nv_bfloat16 *)o, dw, a.cu,
-                  a.n_seq};
+                  a.n_seq, nullptr, 0};
   const dim3 grid((unsigned)(items < device_sms() ? items : device_sms()));
   if (plan) {
     packed_plan(a, p, HEADS ? 128 : 256);

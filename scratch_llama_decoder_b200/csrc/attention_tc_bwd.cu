@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if constexpr (PK) return pk_item(pk, only, item, H, false);
     int z, pr;
     band_item(item, nqb, H * B, z, pr);
-    return Item{nqb - 1 - z, pr % H, pr / H, pr / H * T_all, T_all};
+    return Item{nqb - 1 - z, pr % H, pr / H, pr / H * T_all, T_all, 0};
   };
   // first element of the item's lse and D rows
   auto stat = [&](const Item &im, int h) {
@@ -239,18 +239,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (pk.tiles) pk_wait();  // the plan comes from the kernel before
   }
   const int n_items =
-      PK ? (pk.tiles ? ld_int(pk.n_tiles) * H : only.w * (int)gridDim.x) : nqb * H * B;
+      PK ? (pk.tiles ? ld_int(pk.n_tiles) * H : only.w ? (int)gridDim.x : 0) : nqb * H * B;
 
   if (warp == 0) {
     // ---------------------------------------------- TMA producer (warp)
     int gb = 0, nqd = 0, no = 0;  // key blocks, Q/dO tiles and O tiles issued
     bool ok = true;
-    for (int r = 0, it = 0; ok; r++, it++) {
-      const int item = sched_item(r, G, cta);
-      if (item >= n_items) break;
-      const Item im = decode(item);
+    int item = sched_item(0, G, cta);
+    Item im = {};
+    if (item < n_items) im = decode(item);
+    for (int r = 0, it = 0; ok && item < n_items; r++, it++) {
+      const int next = sched_item(r + 1, G, cta);
+      Item in = {};
+      if (next < n_items) in = decode(next);  // there by the time it is needed
       const int qb = im.blk, h = im.h, T = im.T;
       const int q0 = qb * BQ, row_base = im.row0, g = h / (H / Hkv), slot = it & 1;
+      float lv[4];  // packed: this lane's L, on its way while the slots are waited for
+      if constexpr (PK) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          lv[i] = lane + 32 * i < T - q0 ? lse[stat(im, h) + q0 + lane + 32 * i] : 0.f;
+      }
       // Q, dO into the slot of item it - 2 once it was released
       if (!warp_wait(qd_empty + 8 * slot, ((it >> 1) & 1) ^ 1, abort_sh, gflag)) break;
       if (lane == 0) {
@@ -272,8 +281,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tma_load_3d(smem_u32(sO), &tm_o, 0, h, row_base + q0, o_full);
         if (bulk_l) bulk_load(smem_u32(sNL), lrow, nvalid * 4, o_full);
       }
-      if (!bulk_l)
+      if constexpr (PK) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) sNL[lane + 32 * i] = lv[i];
+      } else if (!bulk_l) {
         for (int i = lane; i < nvalid; i += 32) sNL[i] = lrow[i];
+      }
       mbar_arrive(o_full);
       no = it + 1;
       for (int j = 0; j <= qb; j++) {
@@ -294,6 +307,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         gb++;
       }
+      item = next;
+      im = in;
     }
     // every copy this warp issued has landed before the CTA may exit
     if (lane == 0) {
@@ -328,8 +343,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     bool ok = true;
     int gb = 0;
     int item = sched_item(0, G, cta);
+    int nj = 0;
     if (item < n_items) {  // products of the first block
       const int qb = decode(item).blk;
+      nj = qb + 1;
       ok = warp_wait(qd_full, 0, abort_sh, gflag) && warp_wait(b_full, 0, abort_sh, gflag);
       if (ok) {
         fence_after();
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     for (int r = 0, it = 0; item < n_items && ok; r++, it++) {
-      const int nj = decode(item).blk + 1, slot = it & 1;
+      const int slot = it & 1;
       const int next = sched_item(r + 1, G, cta);
       const int qb_next = next < n_items ? decode(next).blk : 0;
       for (int j = 0; j < nj && ok; j++, gb++) {
@@ -379,6 +396,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mma_commit_e(dq_done + 8 * x);
       }
       item = next;
+      nj = qb_next + 1;
     }
     mma_commit_e(drain + 8 * x);
     if (lane == 0) drain_wait(drain + 8 * x, 0);
@@ -394,10 +412,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     bool ok = true;
     int gb = 0, st_slot = -1;  // slot whose dQ store is still to be released
     int qr = 0;  // uses of the row groups' exchange (red, qred)
-    for (int rr = 0, it = 0; ok; rr++, it++) {
-      const int item = sched_item(rr, G, cta);
-      if (item >= n_items) break;
-      const Item im = decode(item);
+    int item = sched_item(0, G, cta);
+    Item im = {};
+    if (item < n_items) im = decode(item);
+    Item in = {};
+    int next;
+    for (int rr = 0, it = 0; ok && item < n_items; rr++, it++, item = next, im = in) {
+      next = sched_item(rr + 1, G, cta);
+      if (next < n_items) in = decode(next);
       const int qb = im.blk, h = im.h, b = im.b, T = im.T;
       const int q0 = qb * BQ, nj = qb + 1, slot = it & 1;
       const int qi = q0 + r;
@@ -462,7 +484,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         st_slot = -1;
       }
-      if (!own_d && cq == 0 && valid) Dv[stat(im, h) + qi] = Di;
+      // packed: L goes along, for the dK/dV kernel's bulk copies
+      const int64_t di = PK ? h * pk.stat + ((im.row0 + 3 * im.seq) & ~3) + qi : stat(im, h) + qi;
+      if (!own_d && cq == 0 && valid) Dv[di] = Di;
+      if (PK && cq == 1 && valid) pk.L[di] = -nl2 * (1.f / LOG2E);
       const float2 nl = make_float2(nl2, nl2);
       float2 nd = make_float2(-Di, -Di);
       for (int j = 0; j < nj && ok; j++, gb++) {
@@ -500,7 +525,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             break;
           }
           Di /= part;
-          if (cq == 0 && valid) Dv[stat(im, h) + qi] = Di;
+          if (cq == 0 && valid) Dv[di] = Di;
           nd = make_float2(-Di, -Di);
         }
         if (diag) {  // the causal mask only on the diagonal block
@@ -671,7 +696,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if constexpr (PK) return pk_item(pk, only, item, Hkv, true);
     int kb, pr;
     band_item(item, nkb_all, Hkv * B, kb, pr);
-    return Item{kb, pr % Hkv, pr / Hkv, pr / Hkv * T_all, T_all};
+    return Item{kb, pr % Hkv, pr / Hkv, pr / Hkv * T_all, T_all, 0};
   };
   auto blocks = [&](const Item &im) { return (im.T + BK - 1) / BK; };
 
@@ -710,16 +735,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *tmem_sh;
   if constexpr (PK) pk_wait();  // the plan, and D, come from the kernels before
   const int n_items =
-      PK ? (pk.tiles ? ld_int(pk.n_tiles) * Hkv : only.w * (int)gridDim.x) : nkb_all * Hkv * B;
+      PK ? (pk.tiles ? ld_int(pk.n_tiles) * Hkv : only.w ? (int)gridDim.x : 0) : nkb_all * Hkv * B;
 
   if (warp == 0) {
     // ---------------------------------------------- TMA producer (warp)
     int gs = 0, nkv = 0;  // steps and K/V tiles issued
     bool ok = true;
-    for (int r = 0, it = 0; ok; r++, it++) {
-      const int item = sched_item(r, G, cta);
-      if (item >= n_items) break;
-      const Item im = decode(item);
+    if (PK) asm volatile("fence.proxy.async.global;" ::: "memory");  // D and L, by bulk copies
+    int item = sched_item(0, G, cta);
+    Item im = {};
+    if (item < n_items) im = decode(item);
+    for (int r = 0, it = 0; ok && item < n_items; r++, it++) {
+      const int next = sched_item(r + 1, G, cta);
+      Item in = {};
+      if (next < n_items) in = decode(next);  // there by the time it is needed
       const int kb = im.blk, g = im.h, T = im.T;
       const int k0 = kb * BK, row_base = im.row0, nq = blocks(im) - kb, slot = it & 1;
       if (!warp_wait(kv_empty + 8 * slot, ((it >> 1) & 1) ^ 1, abort_sh, gflag)) break;
@@ -743,33 +772,43 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // the step's L and D rows by bulk copies when 16-byte aligned (T % 4
         // == 0), else by the lanes; queries past T get L = +inf, so their P is
         // 0 (below 2^-125 where the polynomial exponential takes the pair), and D = 0
+        // packed: 128 rows always (those past the sequence are masked)
         const int64_t base =
-            (PK ? hq * pk.n_rows + im.row0 : ((int64_t)im.b * H + hq) * T) + qb * BQ;
+            (PK ? hq * pk.stat + ((im.row0 + 3 * im.seq) & ~3) : ((int64_t)im.b * H + hq) * T) +
+            qb * BQ;
         const int nvalid = min(BQ, T - qb * BQ);
         if (lane == 0) {
-          mbar_arrive_expect_tx(q_full + 8 * s, 2 * TILE_BYTES + (bulk_l ? 8 * nvalid : 0));
+          mbar_arrive_expect_tx(q_full + 8 * s,
+                                2 * TILE_BYTES + (PK ? 8 * BQ : bulk_l ? 8 * nvalid : 0));
           tma_load_3d(smem_u32(sQ + s * TILE_BYTES), &tm_qkv, 0, hq, row_base + qb * BQ,
                       q_full + 8 * s);
           tma_load_3d(smem_u32(sdO + s * TILE_BYTES), &tm_do, 0, hq, row_base + qb * BQ,
                       q_full + 8 * s);
-          if (bulk_l) {
+          if constexpr (PK) {
+            bulk_load(smem_u32(sL + s * 128), pk.L + base, BQ * 4, q_full + 8 * s);
+            bulk_load(smem_u32(sD + s * 128), Dv + base, BQ * 4, q_full + 8 * s);
+          } else if (bulk_l) {
             bulk_load(smem_u32(sL + s * 128), lse + base, nvalid * 4, q_full + 8 * s);
             bulk_load(smem_u32(sD + s * 128), Dv + base, nvalid * 4, q_full + 8 * s);
           }
         }
+        if constexpr (!PK) {
 #pragma unroll
-        for (int i = lane; i < BQ; i += 32) {
-          if (i >= nvalid) {
-            sL[s * 128 + i] = INFINITY;
-            sD[s * 128 + i] = 0.f;
-          } else if (!bulk_l) {
-            sL[s * 128 + i] = lse[base + i];
-            sD[s * 128 + i] = PK ? ld_float(Dv + base + i) : Dv[base + i];
+          for (int i = lane; i < BQ; i += 32) {
+            if (i >= nvalid) {
+              sL[s * 128 + i] = INFINITY;
+              sD[s * 128 + i] = 0.f;
+            } else if (!bulk_l) {
+              sL[s * 128 + i] = lse[base + i];
+              sD[s * 128 + i] = Dv[base + i];
+            }
           }
         }
         mbar_arrive(ld_full + 8 * s);
         gs++;
       }
+      item = next;
+      im = in;
     }
     if (lane == 0) {
       for (int i = max(0, nkv - 2); i < nkv; i++) drain_wait(kv_full + 8 * (i & 1), (i >> 1) & 1);
@@ -800,8 +839,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     bool ok = true;
     int gs = 0;
     int item = sched_item(0, G, cta);
+    int nsteps = 0;
     if (item < n_items) {  // products of the first step
       const Item im = decode(item);
+      nsteps = grp * (blocks(im) - im.blk);
       ok = warp_wait(kv_full, 0, abort_sh, gflag) && warp_wait(q_full, 0, abort_sh, gflag);
       if (ok) {
         fence_after();
@@ -810,8 +851,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     for (int r = 0, it = 0; item < n_items && ok; r++, it++) {
-      const Item im = decode(item);
-      const int nsteps = grp * (blocks(im) - im.blk), slot = it & 1;
+      const int slot = it & 1;
       const int next = sched_item(r + 1, G, cta);
       int nsteps_next = grp;
       if (next < n_items) {
@@ -852,6 +892,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mma_commit_e(pv_done);
       }
       item = next;
+      nsteps = nsteps_next;
     }
     mma_commit_e(drain + 8 * x);
     if (lane == 0) drain_wait(drain + 8 * x, 0);
@@ -865,10 +906,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float sl2 = scale * LOG2E;
     bool ok = true;
     int gs = 0, st_slot = -1;  // slot whose dK/dV stores are still to be released
-    for (int rr = 0, it = 0; ok; rr++, it++) {
-      const int item = sched_item(rr, G, cta);
-      if (item >= n_items) break;
-      const Item im = decode(item);
+    int item = sched_item(0, G, cta), next;
+    Item im = {}, in = {};
+    if (item < n_items) im = decode(item);
+    for (int rr = 0, it = 0; ok && item < n_items; rr++, it++, item = next, im = in) {
+      next = sched_item(rr + 1, G, cta);
+      if (next < n_items) in = decode(next);
       const int kb = im.blk, g = im.h, b = im.b, T = im.T;
       const int k0 = kb * BK, kj = k0 + r, nq = blocks(im) - kb, slot = it & 1;
       const int nsteps = grp * nq;
@@ -1105,9 +1148,8 @@ bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float 
   const bool plan = p.cap * a.H > sms || a.n_seq > PK_FIND_SEQ;  // as in the forward
   const float scale = 1.0f / sqrtf((float)a.hd);
   const PkView pk{p.n_tiles, plan ? p.tiles : nullptr, a.n_rows, (__nv_bfloat16 *)dqkv, dld, a.cu,
-                  a.n_seq};
+                  a.n_seq, p.D + p.stat * a.H, p.stat};
   const dim3 gq((unsigned)min(p.cap * a.H, sms)), gkv((unsigned)min(p.cap * a.Hkv, sms));
-  // L and D rows start anywhere: read by the lanes
   if (plan) {
     packed_plan(a, p, PK_BLOCK);
     launch_dependent(k_attn_dq_tc<true>, gq, dim3(NTHREADS), DQ_SMEM, a.s, mq, md, mo, mst, lse, p.D,

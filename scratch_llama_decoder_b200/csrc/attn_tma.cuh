@@ -35,16 +35,20 @@ struct PkView {
   // without a plan (tiles null): the offsets, one item a block
   const int32_t *cu;
   int n_seq;
+  // backward: L beside D, and the stride of their heads (PkPlan)
+  float *L;
+  int64_t stat;
 };
 // One work item: 128-row block (query or key), head, sequence.
 struct Item {
-  int blk, h, b, row0, T;
+  int blk, h, b, row0, T, seq;
 };
 // (tile: what pk_find gave, for a block's only item)
 LLM_DEV Item pk_item(const PkView &pk, const int4 &tile, int item, int heads, bool keys) {
   const int4 t = pk.tiles ? ld_int4(pk.tiles + item / heads) : tile;
   const int n = (t.y + PK_BLOCK - 1) / PK_BLOCK;
-  return Item{keys ? n - 1 - t.z : t.z, item % heads, 0, t.x, t.y};
+  // (the plan's tiles carry the sequence, pk_find's the sequence + 1)
+  return Item{keys ? n - 1 - t.z : t.z, item % heads, 0, t.x, t.y, pk.tiles ? t.w : t.w - 1};
 }
 // Rows [first, 32) of the 32-row group at `rows` (128-byte rows) to zero, by
 // the 128 threads of the group's four warps (t = 0 .. 127): the rows of a

@@ -13,10 +13,10 @@ constexpr int PK_MAX_SEQ = 65536;         // sequences of one call
 enum : int { PK_BAD_OFFSETS = 1, PK_BAD_PAGE = 2 };
 
 // One tile of a sequence, 128 rows (or 256): first packed row and length of the
-// sequence, block index within it.  As a key tile the same entry stands for
+// sequence, block index within it, the sequence.  As a key tile the same entry stands for
 // block n - 1 - blk (n blocks), whose query blocks are as many.
 struct PkTile {
-  int row0, len, blk, pad;
+  int row0, len, blk, seq;
 };
 // The workspace: tile count, a flag word for callers without one, the counter
 // of a queue of items (cleared by the plan); then the tiles (most work first), then scratch
@@ -25,7 +25,11 @@ struct PkPlan {
   int *n_tiles;
   PkTile *tiles;
   int *off, *rank;
+  // the backward's statistics: [H][n_rows] D, or [2: D, L][H][stat] with every
+  // sequence's first row on 16 bytes (row r of sequence s at (row0 + 3 s) / 4 * 4
+  // + r), for bulk copies of 128 rows
   float *D;
+  int64_t stat;
   int64_t cap, bytes;
 };
 inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward) {
@@ -43,7 +47,8 @@ inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward)
   p.tiles = (PkTile *)take(p.cap * (int64_t)sizeof(PkTile));
   p.off = (int *)take(4 * ((int64_t)n_seq + 1));
   p.rank = (int *)take(4 * (int64_t)n_seq);
-  p.D = (float *)take(backward ? 4 * n_rows * H : 0);
+  p.stat = (n_rows + 3 * (int64_t)n_seq + 256 + 3) / 4 * 4;
+  p.D = (float *)take(backward ? 2 * 4 * p.stat * H : 0);
   p.bytes = at;
   return p;
 }
@@ -51,7 +56,7 @@ inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward)
 // Without a plan, where every block gets one item at most: tile k (in the
 // sequences' order) of `block` rows, found by a whole warp from the offsets
 // themselves, clamped as the plan clamps them.  {first row, length, block,
-// tile exists}.
+// sequence + 1 or 0 for no such tile}.
 LLM_DEV int4 pk_find(const int32_t *cu, int n_seq, int n_rows, int block, int k, int *flag) {
   const int lane = threadIdx.x & 31;
   int top = 0;  // the largest offset so far
@@ -77,7 +82,7 @@ LLM_DEV int4 pk_find(const int32_t *cu, int n_seq, int n_rows, int block, int k,
     if (hit) {
       const int src = __ffs(hit) - 1;
       return make_int4(__shfl_sync(0xffffffffu, lo, src), __shfl_sync(0xffffffffu, hi - lo, src),
-                       __shfl_sync(0xffffffffu, k - (n - own), src), 1);
+                       __shfl_sync(0xffffffffu, k - (n - own), src), s0 + src + 1);
     }
     k -= __shfl_sync(0xffffffffu, n, 31);
     top = __shfl_sync(0xffffffffu, hi, 31);
