@@ -45,8 +45,7 @@ using namespace attn_maps;
 
 constexpr int SUB_BYTES = 128 * 64 * 2;  // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int NTHREADS = 384;
-constexpr int SLOTS = 4;     // items handed out ahead
-constexpr int READERS = 10;  // warps that take items from the producer
+constexpr int SLOTS = 2;  // items handed out ahead
 constexpr int TMEM_COLS = 512;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LAZY = 8.f;  // log2 units a row maximum may grow before O is rescaled
@@ -57,29 +56,36 @@ template <int HD>
 struct Cfg {
   static constexpr int SUB = HD / 64, TILE = SUB * SUB_BYTES;
   static constexpr bool SEP = HD == 64;
-  static constexpr int QS = HD == 64 ? 2 : 1;   // Q slots of a stream
-  static constexpr int KST = HD == 64 ? 3 : 2;  // K and V ring stages
-  static constexpr int SMEM = (2 * QS + 2 * KST) * TILE + BAR_BYTES + 1024;
+  static constexpr bool ALONE = HD == 64;      // streams with items, K and V of their own
+  static constexpr int QS = HD == 64 ? 2 : 1;  // Q slots of a stream
+  static constexpr int KST = 2;                // K and V ring stages
+  static constexpr int RINGS = ALONE ? 2 : 1;  // K and V rings, item queues
+  static constexpr int READERS = ALONE ? 5 : 10;  // warps that take items from a producer
+  static constexpr int SMEM = (2 * QS + 2 * KST * RINGS) * TILE + BAR_BYTES + 1024;
   // TMEM columns
   static constexpr int S(int x) { return 128 * x; }
   static constexpr int O(int x) { return 256 + HD * x; }
   static constexpr int P(int x) { return SEP ? 384 + 64 * x : 128 * x; }
 };
 
-// An item: what the streams do.
+// An item: what the streams do (ALONE: the same for the one that took it).
 struct Work {
   int row0, T, g;    // sequence, kv head
   int q[2], h[2];    // row block (of 128) and head of each stream
   int n[2], nj;      // key blocks of each stream (0: no rows), of the item
 };
 // t: the item's index and its tile (first row, length, block).
-template <bool HEADS>
+template <bool ALONE, bool HEADS>
 LLM_DEV Work work(int4 t, int H, int Hkv) {
   const int i = t.x % (HEADS ? H / 2 : H), grp = H / Hkv;
   Work w;
   w.row0 = t.y;
   w.T = t.z;
-  if (HEADS) {
+  if (ALONE) {
+    w.h[0] = w.h[1] = i;
+    w.q[0] = w.q[1] = t.w;
+    w.n[0] = w.n[1] = t.w + 1;
+  } else if (HEADS) {
     w.h[0] = 2 * i;
     w.h[1] = 2 * i + 1;
     w.q[0] = w.q[1] = t.w;
@@ -132,19 +138,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   using C = Cfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sQ = smem, *sK = sQ + 2 * C::QS * C::TILE, *sV = sK + C::KST * C::TILE;
-  uint64_t *bars = (uint64_t *)(sV + C::KST * C::TILE);
+  constexpr int RING = C::KST * C::TILE;  // bytes of a K or V ring
+  uint8_t *sQ = smem, *sK = sQ + 2 * C::QS * C::TILE, *sV = sK + C::RINGS * RING;
+  uint64_t *bars = (uint64_t *)(sV + C::RINGS * RING);
   uint32_t *tmem_sh = (uint32_t *)(bars + 48);
   volatile int *abort_sh = (volatile int *)(tmem_sh + 1);
-  int4 *items = (int4 *)(bars + 50);  // [SLOTS]
+  int4 *items = (int4 *)(bars + 50);  // [ring][SLOTS]
   const uint32_t b0 = smem_u32(bars);
   const uint32_t q_full = b0, q_empty = q_full + 16 * C::QS,  // [stream][slot]
-                 k_full = q_empty + 16 * C::QS, k_empty = k_full + 8 * C::KST,
-                 v_full = k_empty + 8 * C::KST, v_empty = v_full + 8 * C::KST,
-                 s_full = v_empty + 8 * C::KST, s_free = s_full + 16, p_full = s_free + 16,
+                 s_full = q_empty + 16 * C::QS, s_free = s_full + 16, p_full = s_free + 16,
                  o_done = p_full + 16, drain = o_done + 16,  // [stream] each
-                 i_full = drain + 16, i_empty = i_full + 8 * SLOTS;
-  static_assert(4 * C::QS + 4 * C::KST + 10 + 2 * SLOTS <= 48 && 400 + 16 * SLOTS <= BAR_BYTES,
+                 rings = drain + 16;                         // per ring: see below
+  constexpr int RING_BARS = 4 * C::KST + 2 * SLOTS;
+  static_assert(4 * C::QS + 10 + C::RINGS * RING_BARS <= 48 &&
+                    400 + 16 * C::RINGS * SLOTS <= BAR_BYTES,
                 "barriers overlap the TMEM address word or the items");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
@@ -154,11 +161,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1 + 4);  // the last S product; each warp's part of O stored
     }
-    for (int s = 0; s < C::KST; s++) {
-      mbar_init(k_full + 8 * s, 1);
-      mbar_init(k_empty + 8 * s, 2);  // both streams
-      mbar_init(v_full + 8 * s, 1);
-      mbar_init(v_empty + 8 * s, 2);
+    for (int i = 0; i < C::RINGS; i++) {
+      const uint32_t k_full = rings + 8 * RING_BARS * i, k_empty = k_full + 8 * C::KST,
+                     v_full = k_empty + 8 * C::KST, v_empty = v_full + 8 * C::KST,
+                     i_full = v_empty + 8 * C::KST, i_empty = i_full + 8 * SLOTS;
+      for (int s = 0; s < C::KST; s++) {
+        mbar_init(k_full + 8 * s, 1);
+        mbar_init(k_empty + 8 * s, 2 / C::RINGS);  // every stream of the ring
+        mbar_init(v_full + 8 * s, 1);
+        mbar_init(v_empty + 8 * s, 2 / C::RINGS);
+      }
+      for (int s = 0; s < SLOTS; s++) {
+        mbar_init(i_full + 8 * s, 1);
+        mbar_init(i_empty + 8 * s, C::READERS);
+      }
     }
     for (int x = 0; x < 2; x++) {
       mbar_init(s_full + 8 * x, 1);
@@ -166,10 +182,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(p_full + 8 * x, 4);
       mbar_init(o_done + 8 * x, 1);
       mbar_init(drain + 8 * x, 1);
-    }
-    for (int i = 0; i < SLOTS; i++) {
-      mbar_init(i_full + 8 * i, 1);
-      mbar_init(i_empty + 8 * i, READERS);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -185,7 +197,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   fence_after();
   const uint32_t tmem = *tmem_sh;
   if (pk.tiles) pk_wait();  // the plan comes from the kernel before
-  // The it-th item of this CTA, from the producer; t.x < 0: no more (or a wait
+  // the ring of this warp's stream: barriers, K, V, items
+  const int stream = warp == 0 || warp == 1 ? 0 : warp == 2 || warp == 3 ? 1 : (warp - 4) >> 2;
+  const int ring = C::ALONE ? stream : 0;
+  const uint32_t k_full = rings + 8 * RING_BARS * ring, k_empty = k_full + 8 * C::KST,
+                 v_full = k_empty + 8 * C::KST, v_empty = v_full + 8 * C::KST,
+                 i_full = v_empty + 8 * C::KST, i_empty = i_full + 8 * SLOTS;
+  sK += ring * RING;
+  sV += ring * RING;
+  items += ring * SLOTS;
+  // The it-th item of this warp's stream, from the producer; t.x < 0: no more (or a wait
   // gave up).  Whole warps; each takes every item once.
   auto take = [&](int it) {
     int4 t = make_int4(-1, 0, 0, 0);
@@ -198,17 +219,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     return t;
   };
 
-  if (warp == 0) {
-    const int heads = HEADS ? H / 2 : H;
+  if (warp == 0 || (C::ALONE && warp == 3)) {
+    constexpr int BLOCK = C::ALONE || HEADS ? 128 : 256;  // rows of the plan's tiles
+    const int heads = !C::ALONE && HEADS ? H / 2 : H;
     int4 only = make_int4(0, 0, 0, 0);
     if (!pk.tiles)
-      only = pk_find(pk.cu, pk.n_seq, (int)pk.n_rows, HEADS ? 128 : 256, blockIdx.x / heads, gflag);
+      only = pk_find(pk.cu, pk.n_seq, (int)pk.n_rows, BLOCK, blockIdx.x / heads, gflag);
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
       int gb = 0, nq[2] = {0, 0};  // key blocks, Q tiles of each stream issued
       bool ok = true;
       const int n_items = pk.tiles ? ld_int(pk.n_tiles) * heads : only.w ? gridDim.x : 0;
-      int item = blockIdx.x;
+      // (no plan: one item a block, the first stream's)
+      int item = ring * gridDim.x + blockIdx.x;
       for (int it = 0;; it++) {
         int4 t = make_int4(-1, 0, 0, 0);
         if (item < n_items) {
@@ -221,9 +244,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_arrive(i_full + 8 * is);
         if (t.x < 0) break;
         // the next item, from the queue, while this one's tiles are loaded
-        item = pk.tiles ? gridDim.x + atomicAdd(pk.n_tiles + 2, 1) : n_items;
-        const Work w = work<HEADS>(t, H, Hkv);
-        for (int x = 0; x < 2 && ok; x++) {
+        item = pk.tiles ? C::RINGS * gridDim.x + atomicAdd(pk.n_tiles + 2, 1) : n_items;
+        const Work w = work<C::ALONE, HEADS>(t, H, Hkv);
+        for (int x = C::ALONE ? stream : 0; x < (C::ALONE ? stream + 1 : 2) && ok; x++) {
           if (w.n[x] == 0) continue;
           const int sl = nq[x] % C::QS;
           const uint32_t bar = 8 * (x * C::QS + sl);
@@ -281,7 +304,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int it = 0; ok; it++) {
       const int4 t = take(it);
       if (t.x < 0) break;
-      const Work w = work<HEADS>(t, H, Hkv);
+      const Work w = work<C::ALONE, HEADS>(t, H, Hkv);
       const int n = w.n[x];
       const uint32_t qb = 8 * (x * C::QS + nq % C::QS);
       const uint64_t qd = sdesc(smem_u32(sQ + (x * C::QS + nq % C::QS) * C::TILE), 16, 1024);
@@ -352,7 +375,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int it = 0; ok; it++) {
       const int4 t = take(it);
       if (t.x < 0) break;
-      const Work w = work<HEADS>(t, H, Hkv);
+      const Work w = work<C::ALONE, HEADS>(t, H, Hkv);
       const int n = w.n[x], q0 = w.q[x] * 128, T = w.T;
       if (n == 0) {
         gb += w.nj;
@@ -536,7 +559,8 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
   if (!head_map_load(&map, a.qkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, a.ld, 128) ||
       !head_map_store(&mo, o, a.hd, a.H, a.n_rows, 1, dw, 32))
     return false;
-  const int64_t items = p.cap * (HEADS ? a.H / 2 : a.H);
+  constexpr bool PAIRS = !Cfg<HD>::ALONE && HEADS;
+  const int64_t items = p.cap * (PAIRS ? a.H / 2 : a.H);
   // one item a block at most: no order to plan (17 rows, 8 heads: 10.3 us with
   // the plan's kernel, 8.9 without)
   const bool plan = items > device_sms() || a.n_seq > PK_FIND_SEQ;
@@ -544,7 +568,7 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
                   a.n_seq, nullptr, 0};
   const dim3 grid((unsigned)(items < device_sms() ? items : device_sms()));
   if (plan) {
-    packed_plan(a, p, HEADS ? 128 : 256);
+    packed_plan(a, p, Cfg<HD>::ALONE || HEADS ? 128 : 256);
     launch_dependent(kern, grid, dim3(NTHREADS), Cfg<HD>::SMEM, a.s, map, mo, lse, a.H, a.Hkv, a.hd,
                      1.0f / sqrtf((float)a.hd), pk, flag);
   } else {
@@ -563,7 +587,7 @@ bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
   const bool heads = (a.H / a.Hkv) % 2 == 0;
   if (a.hd > 64)
     return heads ? launch<128, true>(a, p, o, lse, flag) : launch<128, false>(a, p, o, lse, flag);
-  return heads ? launch<64, true>(a, p, o, lse, flag) : launch<64, false>(a, p, o, lse, flag);
+  return launch<64, false>(a, p, o, lse, flag);
 }
 
 }  // namespace llm
