@@ -55,11 +55,11 @@ LLM_DEV int block_scan(int v, int *warp_tot) {
 __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int n_seq, int n_rows,
                                              int *__restrict__ n_tiles, PkTile *__restrict__ tiles,
                                              int *__restrict__ off, int *__restrict__ rank,
-                                             int block, int *flag) {
+                                             int *flag) {
   __shared__ int hist[MAXC + 2];  // sequences of exactly n blocks; then cnt, then off
   pk_release();
   __shared__ int warp_tot[32];
-  const int C = (n_rows + block - 1) / block;
+  const int C = (n_rows + PK_BLOCK - 1) / PK_BLOCK;
   for (int i = threadIdx.x; i <= C + 1; i += PT) hist[i] = 0;
   // offsets: running maximum of the clamped entries
   int carry = 0;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
   if (bad && flag) atomicOr(flag, PK_BAD_OFFSETS);
   __syncthreads();
   for (int s = threadIdx.x; s < n_seq; s += PT) {
-    const int n = (off[s + 1] - off[s] + block - 1) / block;
+    const int n = (off[s + 1] - off[s] + PK_BLOCK - 1) / PK_BLOCK;
     // the rank among sequences of as many blocks, completed below
     rank[s] = n ? atomicAdd(&hist[n], 1) : 0;
   }
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
   if (threadIdx.x == 0) hist[C + 1] = 0;
   __syncthreads();
   for (int s = threadIdx.x; s < n_seq; s += PT) {
-    const int n = (off[s + 1] - off[s] + block - 1) / block;
+    const int n = (off[s + 1] - off[s] + PK_BLOCK - 1) / PK_BLOCK;
     if (n) rank[s] += hist[n + 1];  // after every longer sequence
   }
   __syncthreads();
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
   }
   __syncthreads();
   for (int s = threadIdx.x >> 5; s < n_seq; s += PT / 32) {
-    const int row0 = off[s], len = off[s + 1] - row0, n = (len + block - 1) / block;
+    const int row0 = off[s], len = off[s + 1] - row0, n = (len + PK_BLOCK - 1) / PK_BLOCK;
     for (int b = threadIdx.x & 31; b < n; b += 32)
       tiles[hist[b + 1] + rank[s]] = PkTile{row0, len, b, s};
   }
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(PT) k_plan(const int32_t *__restrict__ cu, int
 constexpr int FEW = 256;
 __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu, int n_seq,
                                                   int n_rows, int *__restrict__ n_tiles,
-                                                  PkTile *__restrict__ tiles, int block, int *flag) {
+                                                  PkTile *__restrict__ tiles, int *flag) {
   __shared__ int off[FEW + 1], blocks[FEW], rank[FEW], base[MAXC + 1];
   __shared__ int warp_tot[FEW / 32];
   pk_release();
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
     if (t == 0) off[n_seq] = max(off[n_seq - 1], min(max(last, 0), n_rows));
     __syncthreads();
   }
-  const int n = t < n_seq ? (off[t + 1] - off[t] + block - 1) / block : 0;
+  const int n = t < n_seq ? (off[t + 1] - off[t] + PK_BLOCK - 1) / PK_BLOCK : 0;
   if (t < n_seq) blocks[t] = n;
   __syncthreads();
   if (t < n_seq) {
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
     for (int s = 0; s < n_seq; s++) r += blocks[s] > n || (blocks[s] == n && s < t);
     rank[t] = r;
   }
-  const int C = (n_rows + block - 1) / block;
+  const int C = (n_rows + PK_BLOCK - 1) / PK_BLOCK;
   for (int c = t; c <= C; c += FEW) {
     int sum = 0;
     for (int s = 0; s < n_seq; s++) sum += max(0, blocks[s] - c);
@@ -596,21 +596,21 @@ static bool vec4(const PkArgs &a, const void *p) {
 
 }  // namespace pk
 
-void packed_plan(const PkArgs &a, const PkPlan &p, int block) {
+void packed_plan(const PkArgs &a, const PkPlan &p) {
   if (a.n_seq <= pk::FEW) {
     pk::k_plan_few<<<1, pk::FEW, 0, a.s>>>(a.cu, a.n_seq, (int)a.n_rows, p.n_tiles, p.tiles,
-                                           block, a.flag);
+                                           a.flag);
     count_launch();
     return;
   }
   pk::k_plan<<<1, pk::PT, 0, a.s>>>(a.cu, a.n_seq, (int)a.n_rows, p.n_tiles, p.tiles, p.off,
-                                    p.rank, block, a.flag);
+                                    p.rank, a.flag);
   count_launch();
 }
 
 bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse) {
   using namespace pk;
-  if (pk_planned(a, p)) packed_plan(a, p, PK_BLOCK);
+  if (pk_planned(a, p)) packed_plan(a, p);
   const bool v = vec4(a, a.qkv);
   if (a.dt == DT_BF16) {
     using T = __nv_bfloat16;
@@ -625,7 +625,7 @@ bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse) {
 bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                      const void *dout, void *dqkv, int64_t dld) {
   using namespace pk;
-  if (pk_planned(a, p)) packed_plan(a, p, PK_BLOCK);
+  if (pk_planned(a, p)) packed_plan(a, p);
   const bool v = vec4(a, a.qkv) && vec4(a, dout);
   if (a.dt == DT_BF16) {
     using T = __nv_bfloat16;

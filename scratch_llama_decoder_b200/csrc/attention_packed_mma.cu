@@ -342,7 +342,7 @@ bool packed_bwd_mma(const PkArgs &a, const PkPlan &p, const void *o, const float
     return false;
   if (!smem_optin((const void *)k_dq, DQ_SMEM) || !smem_optin((const void *)k_dkv, DKV_SMEM))
     return false;
-  if (pk_planned(a, p)) packed_plan(a, p, PK_BLOCK);
+  if (pk_planned(a, p)) packed_plan(a, p);
   launch_dependent(k_dq, dim3((unsigned)(2 * p.cap * a.H)), dim3(NT), DQ_SMEM, a.s,
                    (const bf16 *)a.qkv, a.ld, pk_tiles(a, p), (const bf16 *)o, lse,
                    (const bf16 *)dout, p.D, (bf16 *)dqkv, dld, a.n_rows, a.H, a.Hkv, a.hd);

@@ -3,11 +3,9 @@
 // the tiles are 64 or 128 columns wide and zero past the head's own
 // (attn_tma.cuh).
 //
-// One CTA works on two 128-query tiles at once, streams A and B, that share
-// their key and value tiles: two query heads of one kv head at the same rows
-// where a kv head has an even number of them (HEADS), else two consecutive
-// row blocks of one head (a stream may then have one key block less, or no
-// rows).  Per stream and key block of 128:
+// One CTA works on two 128-query tiles at once, streams A and B, each with
+// items (query tile, head), key and value tiles of its own.  Per stream and
+// key block of 128:
 //   S = Q K_j^T         (M 128, N 128; operands K-major in shared memory)
 //   P = 2^(S c - m)     softmax: 4 warps, a thread holds one row whole
 //   O += P V_j          (M 128, N head size; A = P from TMEM, V MN-major)
@@ -22,15 +20,19 @@
 // threads a row (16 softmax warps, 13% slower on long sequences), the streams
 // taking turns at the exponentials (8%), weights formed on the old maximum
 // while the block's own is found (17%).
-// Items go to the CTAs from a queue, most work first (the plan clears its
-// counter); dealt in a fixed snake the fullest CTA had 6% more at 24 sequences
-// of 16001 rows in all.
+// Items go to the streams from a queue, most work first (the plan clears its
+// counter): dealt in a fixed snake the fullest CTA had 6% more at 24 sequences
+// of 16001 rows in all; streams that share K and V (two heads of a kv head, or
+// two blocks of a head) leave one idle where a sequence is short: 16 heads
+// ragged 119 us against 115, 17 rows 8.9 against 7.3.
+// Measured (heads of 64; 128): 2 documents of 16384 rows in all, 8 heads, 224
+// us, 629 TFLOP/s; 2 x 8192 rows, 280 us, 982 TFLOP/s.
 // TMEM: S_A, S_B (128 columns each), O_A, O_B (head size each).  Heads to 64
 // leave room for P beside S (SEP), so S_{j+1} is computed while block j's
 // softmax runs; at head 128 P takes the first half of S's columns, and S_{j+1}
 // follows O += P V_j.
-// Warps: 0 TMA producer; 1, 2 MMA issuers of A and B (warp 1 also TMEM);
-// 4-7 and 8-11 softmax of A and B.  Every wait is bounded (FLAG_TIMEOUT).
+// Warps: 0, 3 TMA producers of A and B; 1, 2 their MMA issuers (warp 1 also
+// TMEM); 4-7 and 8-11 their softmax.  Every wait is bounded (FLAG_TIMEOUT).
 // Rows of a tile past its sequence's end are another's: masked as keys, zeroed
 // in V before they meet a zero weight, not stored.
 #include "attn_tma.cuh"
@@ -45,7 +47,8 @@ using namespace attn_maps;
 
 constexpr int SUB_BYTES = 128 * 64 * 2;  // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int NTHREADS = 384;
-constexpr int SLOTS = 2;  // items handed out ahead
+constexpr int SLOTS = 2;    // items handed out ahead
+constexpr int READERS = 5;  // warps of a stream that take items from its producer
 constexpr int TMEM_COLS = 512;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LAZY = 8.f;  // log2 units a row maximum may grow before O is rescaled
@@ -56,50 +59,23 @@ template <int HD>
 struct Cfg {
   static constexpr int SUB = HD / 64, TILE = SUB * SUB_BYTES;
   static constexpr bool SEP = HD == 64;
-  static constexpr bool ALONE = HD == 64;      // streams with items, K and V of their own
-  static constexpr int QS = HD == 64 ? 2 : 1;  // Q slots of a stream
-  static constexpr int KST = 2;                // K and V ring stages
-  static constexpr int RINGS = ALONE ? 2 : 1;  // K and V rings, item queues
-  static constexpr int READERS = ALONE ? 5 : 10;  // warps that take items from a producer
-  static constexpr int SMEM = (2 * QS + 2 * KST * RINGS) * TILE + BAR_BYTES + 1024;
+  static constexpr int QS = HD == 64 ? 2 : 1;   // Q slots of a stream
+  static constexpr int KST = HD == 64 ? 2 : 1;  // K and V ring stages of a stream
+  static constexpr int SMEM = (2 * QS + 4 * KST) * TILE + BAR_BYTES + 1024;
   // TMEM columns
   static constexpr int S(int x) { return 128 * x; }
   static constexpr int O(int x) { return 256 + HD * x; }
   static constexpr int P(int x) { return SEP ? 384 + 64 * x : 128 * x; }
 };
 
-// An item: what the streams do (ALONE: the same for the one that took it).
+// An item: query block q (of 128 rows) of a sequence, head h with kv head g, n
+// key blocks.  t: the item's index and its tile (first row, length, block).
 struct Work {
-  int row0, T, g;    // sequence, kv head
-  int q[2], h[2];    // row block (of 128) and head of each stream
-  int n[2], nj;      // key blocks of each stream (0: no rows), of the item
+  int row0, T, q, h, g, n;
 };
-// t: the item's index and its tile (first row, length, block).
-template <bool ALONE, bool HEADS>
 LLM_DEV Work work(int4 t, int H, int Hkv) {
-  const int i = t.x % (HEADS ? H / 2 : H), grp = H / Hkv;
-  Work w;
-  w.row0 = t.y;
-  w.T = t.z;
-  if (ALONE) {
-    w.h[0] = w.h[1] = i;
-    w.q[0] = w.q[1] = t.w;
-    w.n[0] = w.n[1] = t.w + 1;
-  } else if (HEADS) {
-    w.h[0] = 2 * i;
-    w.h[1] = 2 * i + 1;
-    w.q[0] = w.q[1] = t.w;
-    w.n[0] = w.n[1] = t.w + 1;
-  } else {
-    w.h[0] = w.h[1] = i;
-    w.q[0] = 2 * t.w;
-    w.q[1] = 2 * t.w + 1;
-    w.n[0] = 2 * t.w + 1;
-    w.n[1] = w.q[1] * 128 < t.z ? 2 * t.w + 2 : 0;
-  }
-  w.g = w.h[0] / grp;
-  w.nj = max(w.n[0], w.n[1]);
-  return w;
+  const int h = t.x % H;
+  return Work{t.y, t.z, t.w, h, h / (H / Hkv), t.w + 1};
 }
 
 template <int NPAIRS>
@@ -130,28 +106,28 @@ LLM_DEV void tmem_st32u(uint32_t taddr, const uint32_t *w) {
       : "memory");
 }
 
-template <int HD, bool HEADS>
+template <int HD>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    k_attn_fwd_pair(const __grid_constant__ CUtensorMap tm_qkv,
+    k_attn_fwd_streams(const __grid_constant__ CUtensorMap tm_qkv,
                     const __grid_constant__ CUtensorMap tm_o, float *__restrict__ lse, int H,
                     int Hkv, int hd, float scale, const PkView pk, int *gflag) {
   using C = Cfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   constexpr int RING = C::KST * C::TILE;  // bytes of a K or V ring
-  uint8_t *sQ = smem, *sK = sQ + 2 * C::QS * C::TILE, *sV = sK + C::RINGS * RING;
-  uint64_t *bars = (uint64_t *)(sV + C::RINGS * RING);
+  uint8_t *sQ = smem, *sK = sQ + 2 * C::QS * C::TILE, *sV = sK + 2 * RING;
+  uint64_t *bars = (uint64_t *)(sV + 2 * RING);
   uint32_t *tmem_sh = (uint32_t *)(bars + 48);
   volatile int *abort_sh = (volatile int *)(tmem_sh + 1);
-  int4 *items = (int4 *)(bars + 50);  // [ring][SLOTS]
+  int4 *items = (int4 *)(bars + 50);  // [stream][SLOTS]
   const uint32_t b0 = smem_u32(bars);
   const uint32_t q_full = b0, q_empty = q_full + 16 * C::QS,  // [stream][slot]
                  s_full = q_empty + 16 * C::QS, s_free = s_full + 16, p_full = s_free + 16,
                  o_done = p_full + 16, drain = o_done + 16,  // [stream] each
-                 rings = drain + 16;                         // per ring: see below
+                 rings = drain + 16;                         // then each stream's ring
   constexpr int RING_BARS = 4 * C::KST + 2 * SLOTS;
-  static_assert(4 * C::QS + 10 + C::RINGS * RING_BARS <= 48 &&
-                    400 + 16 * C::RINGS * SLOTS <= BAR_BYTES,
+  static_assert(4 * C::QS + 10 + 2 * RING_BARS <= 48 &&
+                    400 + 16 * 2 * SLOTS <= BAR_BYTES,
                 "barriers overlap the TMEM address word or the items");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
@@ -161,19 +137,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1 + 4);  // the last S product; each warp's part of O stored
     }
-    for (int i = 0; i < C::RINGS; i++) {
+    for (int i = 0; i < 2; i++) {
       const uint32_t k_full = rings + 8 * RING_BARS * i, k_empty = k_full + 8 * C::KST,
                      v_full = k_empty + 8 * C::KST, v_empty = v_full + 8 * C::KST,
                      i_full = v_empty + 8 * C::KST, i_empty = i_full + 8 * SLOTS;
       for (int s = 0; s < C::KST; s++) {
         mbar_init(k_full + 8 * s, 1);
-        mbar_init(k_empty + 8 * s, 2 / C::RINGS);  // every stream of the ring
+        mbar_init(k_empty + 8 * s, 1);
         mbar_init(v_full + 8 * s, 1);
-        mbar_init(v_empty + 8 * s, 2 / C::RINGS);
+        mbar_init(v_empty + 8 * s, 1);
       }
       for (int s = 0; s < SLOTS; s++) {
         mbar_init(i_full + 8 * s, 1);
-        mbar_init(i_empty + 8 * s, C::READERS);
+        mbar_init(i_empty + 8 * s, READERS);
       }
     }
     for (int x = 0; x < 2; x++) {
@@ -197,15 +173,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   fence_after();
   const uint32_t tmem = *tmem_sh;
   if (pk.tiles) pk_wait();  // the plan comes from the kernel before
-  // the ring of this warp's stream: barriers, K, V, items
-  const int stream = warp == 0 || warp == 1 ? 0 : warp == 2 || warp == 3 ? 1 : (warp - 4) >> 2;
-  const int ring = C::ALONE ? stream : 0;
-  const uint32_t k_full = rings + 8 * RING_BARS * ring, k_empty = k_full + 8 * C::KST,
+  // this warp's stream: its ring's barriers, K, V, items
+  const int x = warp < 2 ? 0 : warp < 4 ? 1 : (warp - 4) >> 2;
+  const uint32_t k_full = rings + 8 * RING_BARS * x, k_empty = k_full + 8 * C::KST,
                  v_full = k_empty + 8 * C::KST, v_empty = v_full + 8 * C::KST,
                  i_full = v_empty + 8 * C::KST, i_empty = i_full + 8 * SLOTS;
-  sK += ring * RING;
-  sV += ring * RING;
-  items += ring * SLOTS;
+  sK += x * RING;
+  sV += x * RING;
+  items += x * SLOTS;
   // The it-th item of this warp's stream, from the producer; t.x < 0: no more (or a wait
   // gave up).  Whole warps; each takes every item once.
   auto take = [&](int it) {
@@ -219,23 +194,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     return t;
   };
 
-  if (warp == 0 || (C::ALONE && warp == 3)) {
-    constexpr int BLOCK = C::ALONE || HEADS ? 128 : 256;  // rows of the plan's tiles
-    const int heads = !C::ALONE && HEADS ? H / 2 : H;
+  if (warp == 0 || warp == 3) {
     int4 only = make_int4(0, 0, 0, 0);
     if (!pk.tiles)
-      only = pk_find(pk.cu, pk.n_seq, (int)pk.n_rows, BLOCK, blockIdx.x / heads, gflag);
+      only = pk_find(pk.cu, pk.n_seq, (int)pk.n_rows, PK_BLOCK, blockIdx.x / H, gflag);
     if (lane == 0) {
       // ------------------------------------------------------ TMA producer
-      int gb = 0, nq[2] = {0, 0};  // key blocks, Q tiles of each stream issued
+      int gb = 0, nq = 0;  // key blocks, Q tiles issued
       bool ok = true;
-      const int n_items = pk.tiles ? ld_int(pk.n_tiles) * heads : only.w ? gridDim.x : 0;
+      const int n_items = pk.tiles ? ld_int(pk.n_tiles) * H : only.w ? gridDim.x : 0;
       // (no plan: one item a block, the first stream's)
-      int item = ring * gridDim.x + blockIdx.x;
+      int item = x * gridDim.x + blockIdx.x;
       for (int it = 0;; it++) {
         int4 t = make_int4(-1, 0, 0, 0);
         if (item < n_items) {
-          const int4 u = pk.tiles ? ld_int4(pk.tiles + item / heads) : only;
+          const int4 u = pk.tiles ? ld_int4(pk.tiles + item / H) : only;
           t = make_int4(item, u.x, u.y, u.z);
         }
         const int is = it % SLOTS;
@@ -244,21 +217,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_arrive(i_full + 8 * is);
         if (t.x < 0) break;
         // the next item, from the queue, while this one's tiles are loaded
-        item = pk.tiles ? C::RINGS * gridDim.x + atomicAdd(pk.n_tiles + 2, 1) : n_items;
-        const Work w = work<C::ALONE, HEADS>(t, H, Hkv);
-        for (int x = C::ALONE ? stream : 0; x < (C::ALONE ? stream + 1 : 2) && ok; x++) {
-          if (w.n[x] == 0) continue;
-          const int sl = nq[x] % C::QS;
-          const uint32_t bar = 8 * (x * C::QS + sl);
-          ok = mbar_wait(q_empty + bar, ((nq[x] / C::QS) & 1) ^ 1, abort_sh, gflag);
-          if (!ok) break;
-          mbar_arrive_expect_tx(q_full + bar, C::TILE);
-          for (int c = 0; c < C::SUB; c++)
-            tma_load_3d(smem_u32(sQ + (x * C::QS + sl) * C::TILE + c * SUB_BYTES), &tm_qkv, 64 * c,
-                        w.h[x], w.row0 + w.q[x] * 128, q_full + bar);
-          nq[x]++;
-        }
-        for (int j = 0; j < w.nj && ok; j++, gb++) {
+        item = pk.tiles ? 2 * gridDim.x + atomicAdd(pk.n_tiles + 2, 1) : n_items;
+        const Work w = work(t, H, Hkv);
+        const int sl = nq % C::QS;
+        const uint32_t qb = 8 * (x * C::QS + sl);
+        if (!mbar_wait(q_empty + qb, ((nq / C::QS) & 1) ^ 1, abort_sh, gflag)) break;
+        mbar_arrive_expect_tx(q_full + qb, C::TILE);
+        for (int c = 0; c < C::SUB; c++)
+          tma_load_3d(smem_u32(sQ + (x * C::QS + sl) * C::TILE + c * SUB_BYTES), &tm_qkv, 64 * c, w.h,
+                      w.row0 + w.q * 128, q_full + qb);
+        nq++;
+        for (int j = 0; j < w.n && ok; j++, gb++) {
           const int s = gb % C::KST;
           const uint32_t ph = ((gb / C::KST) & 1) ^ 1;
           if (!mbar_wait(k_empty + 8 * s, ph, abort_sh, gflag)) {
@@ -282,17 +251,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!ok) break;
       }
       // every copy this thread issued has landed before the CTA may exit
-      for (int x = 0; x < 2; x++)
-        for (int i = max(0, nq[x] - C::QS); i < nq[x]; i++)
-          drain_wait(q_full + 8 * (x * C::QS + i % C::QS), (i / C::QS) & 1);
+      for (int i = max(0, nq - C::QS); i < nq; i++)
+        drain_wait(q_full + 8 * (x * C::QS + i % C::QS), (i / C::QS) & 1);
       for (int i = max(0, gb - C::KST); i < gb; i++) {
         drain_wait(k_full + 8 * (i % C::KST), (i / C::KST) & 1);
         drain_wait(v_full + 8 * (i % C::KST), (i / C::KST) & 1);
       }
     }
   } else if (warp == 1 || warp == 2) {
-    // ---------------------------------------- MMA issuer of stream x (whole warp)
-    const int x = warp - 1;
+    // ------------------------------------- MMA issuer of the stream (whole warp)
     constexpr uint32_t ID_S = idesc_mn(128, 128, false, false);
     constexpr uint32_t ID_O = idesc_mn(128, HD, false, true);
     int gb = 0, nq = 0, cb = 0;  // the item's first ring block; Q tiles, blocks of the stream
@@ -304,8 +271,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int it = 0; ok; it++) {
       const int4 t = take(it);
       if (t.x < 0) break;
-      const Work w = work<C::ALONE, HEADS>(t, H, Hkv);
-      const int n = w.n[x];
+      const Work w = work(t, H, Hkv);
+      const int n = w.n;
       const uint32_t qb = 8 * (x * C::QS + nq % C::QS);
       const uint64_t qd = sdesc(smem_u32(sQ + (x * C::QS + nq % C::QS) * C::TILE), 16, 1024);
       auto scores = [&](int j) {  // S = Q K_j^T
@@ -322,50 +289,39 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mma_commit_e(k_empty + 8 * s);
         if (j == n - 1) mma_commit_e(q_empty + qb);
       };
-      if (n > 0) {
-        if (!wait(q_full + qb, nq / C::QS)) break;
-        // the buffer of the stream's previous block was read (P V done: P is in it)
-        if (cb > 0 && !wait((C::SEP ? s_free : o_done) + 8 * x, cb - 1)) break;
-        scores(0);
-        for (int j = 0; j < n && ok; j++, cb++) {
-          const int s = (gb + j) % C::KST;
-          if (C::SEP && j + 1 < n) {
-            if (!wait(s_free + 8 * x, cb)) break;
-            scores(j + 1);
-          }
-          if (!wait(v_full + 8 * s, (gb + j) / C::KST) || !wait(p_full + 8 * x, cb)) break;
-          fence_after();
-          const uint64_t vd = sdesc(smem_u32(sV + s * C::TILE), SUB_BYTES, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 8; kk++)
-            mma_ts_e(tmem + C::O(x), tmem + C::P(x) + kk * 8, vd + (uint64_t)(kk * 128), ID_O,
-                     (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_e(o_done + 8 * x);
-          mma_commit_e(v_empty + 8 * s);
-          if (!C::SEP && j + 1 < n) {
-            if (!wait(o_done + 8 * x, cb)) break;
-            scores(j + 1);
-          }
-        }
-        nq++;
-      }
-      // key blocks that only the other stream reads: released once they are
-      // there, so that no arrival can count for an earlier use of the slot
-      for (int j = n; j < w.nj && ok; j++) {
+      if (!wait(q_full + qb, nq / C::QS)) break;
+      // the buffer of the stream's previous block was read (P V done: P is in it)
+      if (cb > 0 && !wait((C::SEP ? s_free : o_done) + 8 * x, cb - 1)) break;
+      scores(0);
+      for (int j = 0; j < n && ok; j++, cb++) {
         const int s = (gb + j) % C::KST;
-        if (!wait(k_full + 8 * s, (gb + j) / C::KST)) break;
-        if (lane == 0) mbar_arrive(k_empty + 8 * s);
-        if (!wait(v_full + 8 * s, (gb + j) / C::KST)) break;
-        if (lane == 0) mbar_arrive(v_empty + 8 * s);
+        if (C::SEP && j + 1 < n) {
+          if (!wait(s_free + 8 * x, cb)) break;
+          scores(j + 1);
+        }
+        if (!wait(v_full + 8 * s, (gb + j) / C::KST) || !wait(p_full + 8 * x, cb)) break;
+        fence_after();
+        const uint64_t vd = sdesc(smem_u32(sV + s * C::TILE), SUB_BYTES, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; kk++)
+          mma_ts_e(tmem + C::O(x), tmem + C::P(x) + kk * 8, vd + (uint64_t)(kk * 128), ID_O,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_e(o_done + 8 * x);
+        mma_commit_e(v_empty + 8 * s);
+        if (!C::SEP && j + 1 < n) {
+          if (!wait(o_done + 8 * x, cb)) break;
+          scores(j + 1);
+        }
       }
-      gb += w.nj;
+      nq++;
+      gb += n;
     }
     mma_commit_e(drain + 8 * x);
     if (lane == 0) drain_wait(drain + 8 * x, 0);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
-    const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::S(x), tP = tmem + lane_off + C::P(x),
                    tO = tmem + lane_off + C::O(x);
@@ -375,12 +331,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int it = 0; ok; it++) {
       const int4 t = take(it);
       if (t.x < 0) break;
-      const Work w = work<C::ALONE, HEADS>(t, H, Hkv);
-      const int n = w.n[x], q0 = w.q[x] * 128, T = w.T;
-      if (n == 0) {
-        gb += w.nj;
-        continue;
-      }
+      const Work w = work(t, H, Hkv);
+      const int n = w.n, q0 = w.q * 128, T = w.T;
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int j = 0; j < n; j++, cb++) {
@@ -482,7 +434,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       if (!ok) break;
-      gb += w.nj;
+      gb += n;
       // O = O / l: through the item's Q tile (its last S product is complete)
       // in the 128-byte-swizzle image of the store's boxes
       if (!(ok = warp_wait(o_done + 8 * x, (cb - 1) & 1, abort_sh, gflag))) break;
@@ -516,7 +468,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (q0 + r0 + 32 <= T) {
         if (lane == 0) {
           for (int c = 0; c < C::SUB; c++)
-            tma_store_4d(&tm_o, smem_u32(tile + c * SUB_BYTES + r0 * 128), 64 * c, w.h[x],
+            tma_store_4d(&tm_o, smem_u32(tile + c * SUB_BYTES + r0 * 128), 64 * c, w.h,
                          w.row0 + q0 + r0, 0);
           bulk_commit();
         }
@@ -524,11 +476,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int rr = r0; rr < r0 + 32; rr += 8)
           for (int c = 0; c < C::SUB; c++)
             store_cut(tile + c * SUB_BYTES, rr, T - q0,
-                      pk.out + (int64_t)(w.row0 + q0 + rr) * pk.out_ld + w.h[x] * hd + 64 * c,
+                      pk.out + (int64_t)(w.row0 + q0 + rr) * pk.out_ld + w.h * hd + 64 * c,
                       pk.out_ld, hd - 64 * c, lane);
       }
       if (q0 + row < T)
-        lse[w.h[x] * pk.n_rows + w.row0 + q0 + row] = (m + __log2f(l)) * LN2;
+        lse[w.h * pk.n_rows + w.row0 + q0 + row] = (m + __log2f(l)) * LN2;
       __syncwarp();
       if (C::QS > 1) {
         st_slot = sl;  // released after the next item's first block
@@ -550,17 +502,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-template <int HD, bool HEADS>
+template <int HD>
 static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag) {
-  auto kern = k_attn_fwd_pair<HD, HEADS>;
+  auto kern = k_attn_fwd_streams<HD>;
   if (!smem_optin((const void *)kern, Cfg<HD>::SMEM)) return false;
   const int64_t dw = (int64_t)a.H * a.hd;
   CUtensorMap map, mo;
   if (!head_map_load(&map, a.qkv, a.hd, a.H + 2 * a.Hkv, a.n_rows, a.ld, 128) ||
       !head_map_store(&mo, o, a.hd, a.H, a.n_rows, 1, dw, 32))
     return false;
-  constexpr bool PAIRS = !Cfg<HD>::ALONE && HEADS;
-  const int64_t items = p.cap * (PAIRS ? a.H / 2 : a.H);
+  const int64_t items = p.cap * a.H;
   // one item a block at most: no order to plan (17 rows, 8 heads: 10.3 us with
   // the plan's kernel, 8.9 without)
   const bool plan = items > device_sms() || a.n_seq > PK_FIND_SEQ;
@@ -568,7 +519,7 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
                   a.n_seq, nullptr, 0};
   const dim3 grid((unsigned)(items < device_sms() ? items : device_sms()));
   if (plan) {
-    packed_plan(a, p, Cfg<HD>::ALONE || HEADS ? 128 : 256);
+    packed_plan(a, p);
     launch_dependent(kern, grid, dim3(NTHREADS), Cfg<HD>::SMEM, a.s, map, mo, lse, a.H, a.Hkv, a.hd,
                      1.0f / sqrtf((float)a.hd), pk, flag);
   } else {
@@ -584,10 +535,7 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
 bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag) {
   using namespace attn_pk_tc;
   if (a.dt != DT_BF16 || a.hd % 8) return false;
-  const bool heads = (a.H / a.Hkv) % 2 == 0;
-  if (a.hd > 64)
-    return heads ? launch<128, true>(a, p, o, lse, flag) : launch<128, false>(a, p, o, lse, flag);
-  return launch<64, false>(a, p, o, lse, flag);
+  return a.hd > 64 ? launch<128>(a, p, o, lse, flag) : launch<64>(a, p, o, lse, flag);
 }
 
 }  // namespace llm

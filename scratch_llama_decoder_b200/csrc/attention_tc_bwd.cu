@@ -1151,7 +1151,7 @@ bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float 
                   a.n_seq, p.D + p.stat * a.H, p.stat};
   const dim3 gq((unsigned)min(p.cap * a.H, sms)), gkv((unsigned)min(p.cap * a.Hkv, sms));
   if (plan) {
-    packed_plan(a, p, PK_BLOCK);
+    packed_plan(a, p);
     launch_dependent(k_attn_dq_tc<true>, gq, dim3(NTHREADS), DQ_SMEM, a.s, mq, md, mo, mst, lse, p.D,
                      (__nv_bfloat16 *)dqkv, nullptr, nullptr, 1, 0, a.H, a.Hkv, a.hd, scale, 0, pk,
                      flag);

@@ -12,8 +12,8 @@ constexpr int PK_MAX_SEQ = 65536;         // sequences of one call
 // bits OR-ed into the caller's flag word (FLAG_TIMEOUT is bit 4)
 enum : int { PK_BAD_OFFSETS = 1, PK_BAD_PAGE = 2 };
 
-// One tile of a sequence, 128 rows (or 256): first packed row and length of the
-// sequence, block index within it, the sequence.  As a key tile the same entry stands for
+// One 128-row tile of a sequence: first packed row and length of the sequence,
+// block index within it, the sequence.  As a key tile the same entry stands for
 // block n - 1 - blk (n blocks), whose query blocks are as many.
 struct PkTile {
   int row0, len, blk, seq;
@@ -136,8 +136,8 @@ inline bool pk_planned(const PkArgs &a, const PkPlan &p) {
 inline PkTiles pk_tiles(const PkArgs &a, const PkPlan &p) {
   return PkTiles{p.n_tiles, pk_planned(a, p) ? p.tiles : nullptr, a.cu, a.n_seq, (int)a.n_rows, a.flag};
 }
-// Enqueues the plan; block: rows of a tile, 128 or 256.
-void packed_plan(const PkArgs &a, const PkPlan &p, int block);
+// Enqueues the plan.
+void packed_plan(const PkArgs &a, const PkPlan &p);
 // tcgen05 kernels (with their plan): bfloat16, head sizes that are multiples of
 // 8 (to 128 forward, to 64 backward), rows that start on 16 bytes; false
 // (nothing launched) otherwise.  flag:
