@@ -146,8 +146,9 @@ int llm_kernel_embed_bwd_noalloc(const int32_t *d_tokens, const float *d_dx, flo
  *     nothing outside the rows is touched -- and bit 4 (LLM_PACKED_TIMEOUT)
  *     when a bounded wait of the tensor-core kernels gave up (the outputs are
  *     incomplete).  Never cleared here.
- * A value that is not finite reaches rows of its own sequence only: those
- * behind it, and of those before it any in the same 128 rows of the sequence.
+ * A value that is not finite reaches rows of its own sequence only: in the
+ * forward those behind it, and of those before it any in the same 128 rows of
+ * the sequence; in the backward any of them.
  * Limits: n_rows <= 2^20, n_seq <= 65536, n_head <= 1024, an even head_dim of
  * 2 to 128.  n_rows = 0 or n_seq = 0 launches nothing.  LLM_ERR_ARG outside
  * them, for a null or misaligned pointer or a small workspace.  Asynchronous
@@ -170,7 +171,8 @@ int llm_kernel_attention_packed_bwd(const void *d_qkv, int64_t ld, int dtype, co
  * lengths share pages, and the values may be held in 8 bits.
  *   d_pages: [n_pages][2: k, v][n_kv_head][page_size][head_dim] elements of
  *     `format`; d_scales: float32 [n_pages][2][n_kv_head][page_size], one per
- *     row of head_dim elements, for the 8-bit formats (ignored otherwise).
+ *     row of head_dim elements and not negative, for the 8-bit formats
+ *     (ignored otherwise).
  *   d_table: int32, row s (at d_table + s * table_ld) holds the pages of
  *     sequence s in order: position p is row p % page_size of page
  *     d_table[s * table_ld + p / page_size].  table_pages entries a row.

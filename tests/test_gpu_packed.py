@@ -357,3 +357,127 @@ def test_refused_arguments():
         P.attention_packed_backward(qkv, cu, 4, 2, out, lse[:3], out)
     with pytest.raises(P.LLMError):
         P.attention_packed_backward(qkv, cu, 4, 2, out, lse, out, dqkv=qkv)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_many_sequences_against_the_formulas(hd, dtype):
+    """More sequences than one pass of the plan's search takes, both passes."""
+    gen = torch.Generator().manual_seed(16)
+    lens = torch.randint(0, 30, (400,), generator=gen).tolist() + [700, 0, 131]
+    qkv, dout, cu, cut = _data(lens, 2, 1, hd, dtype, seed=16)
+    _check(qkv, dout, cu, cut, 2, 1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [64, 128, 20])
+@pytest.mark.parametrize("n_seq", [12, 256, 600])
+def test_bad_offsets_of_many_rows(n_seq, hd, dtype):
+    """Bad offsets where the work is planned ahead (few and many sequences):
+    as for the mended offsets, and nothing outside the rows written."""
+    import scratch_llama_decoder_b200 as P
+    h, g, n = 8, 2, 6000
+    gen = torch.Generator().manual_seed(17)
+    qkv, dout, _, _ = _data([n], h, g, hd, dtype, seed=17)
+    good = torch.sort(torch.randint(0, n + 1, (n_seq + 1,), generator=gen))[0].tolist()
+    bad = list(good)
+    bad[3], good[3] = -7, good[2]
+    good[-2:] = [n, n]
+    bad[-2:] = [(1 << 31) - 1, -(1 << 31)]
+    at = n_seq // 2
+    bad[at] = 0
+    good[at] = good[at - 1]
+    wide = (h + 2 * g) * hd
+    res = []
+    for cu in (bad, good):
+        store = torch.full((n + 512, wide), 5.0, device="cuda").to(dtype)
+        out = torch.full((n + 512, h * hd), 5.0, device="cuda").to(dtype)
+        lse = torch.full((h, n), 5.0, device="cuda")
+        cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        flags = torch.zeros(2, dtype=torch.int32, device="cuda")
+        P.attention_packed(qkv, cut, h, g, out=out[256:-256], lse=lse, flag=flags[:1])
+        P.attention_packed_backward(qkv, cut, h, g, out[256:-256], lse, dout,
+                                    dqkv=store[256:-256], flag=flags[1:])
+        assert flags.tolist() == [int(cu is bad)] * 2
+        for x in (out, store):
+            assert bool((x[:256] == 5).all() and (x[-256:] == 5).all())
+        res.append((out, lse, store))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_most_rows_and_sequences(dtype):
+    """The limits, in rows so far apart that offsets pass 2^31 elements: the
+    same bits as in calls of 1024 sequences each on rows next to another."""
+    import scratch_llama_decoder_b200 as P
+    h, g, hd, n, part = 1, 1, 32, 1 << 20, 1 << 14
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    wide = torch.empty(n, 2112, dtype=dtype, device="cuda")
+    qkv, dqkv = wide[:, 1000:1096], wide[:, 1200:1296]
+    qkv.copy_(torch.randn(n, 96, generator=gen, device="cuda"))
+    dout = torch.randn(n, hd, generator=gen, device="cuda").to(dtype)
+    cut = torch.arange(0, n + 1, 16, dtype=torch.int32, device="cuda")
+    out, lse = P.attention_packed(qkv, cut, h, g)
+    P.attention_packed_backward(qkv, cut, h, g, out, lse, dout, dqkv=dqkv)
+    for a in range(0, n, part):
+        x = qkv[a:a + part].contiguous()
+        o, l = P.attention_packed(x, cut[:part // 16 + 1], h, g)
+        assert torch.equal(o, out[a:a + part]) and torch.equal(l, lse[:, a:a + part])
+        d = P.attention_packed_backward(x, cut[:part // 16 + 1], h, g, o, l, dout[a:a + part])
+        assert torch.equal(d, dqkv[a:a + part])
+
+
+def test_longest_sequence():
+    """One sequence of 2^20 rows: rows of the output and of dq, and the last
+    keys' gradients, against the formulas."""
+    import scratch_llama_decoder_b200 as P
+    hd, n = 32, 1 << 20
+    qkv, dout, cu, cut = _data([n], 1, 1, hd, torch.bfloat16, seed=19)
+    out, lse = P.attention_packed(qkv, cut, 1, 1)
+    dx = P.attention_packed_backward(qkv, cut, 1, 1, out, lse, dout)
+    q, k, v = (t[:, 0] for t in ref.split(qkv, 1, 1))
+    r, u, c = 2.0 ** -8, ref.U, 1 / math.sqrt(hd)
+    for i in (0, 127, 128, 77777, n - 2, n - 1):
+        s = k[:i + 1] @ q[i] * c
+        L = torch.logsumexp(s, 0)
+        p = torch.exp(s - L)
+        o, m = p @ v[:i + 1], p @ v[:i + 1].abs()
+        # as packed_ref.attention: scores to (hd + 5) u |q||k|, weights 2^-12 and
+        # rounded; m terms of a sum to u each
+        es = float(((hd + 5) * u * (k[:i + 1].abs() @ q[i].abs()) * c).max()) + 2.0 ** -12
+        rel = 2 * es + (2 * i + 18) * u + r
+        ref.check(lse[0, i], L, es + (i + 9) * u + 4 * u * L.abs(), "lse")
+        ref.check(out[i], o, rel * m + r * o.abs() + 1e-30, "out")
+        do = dout[i].double()
+        dP = v[:i + 1] @ do
+        ds = p * (dP - p @ dP)
+        bD = do.abs() @ (rel * m + r * o.abs())
+        eds = (p * (bD + 2 * es * (dP - p @ dP).abs() + (hd + 2) * u * (v[:i + 1].abs() @ do.abs()))
+               + (r + (i + 9) * u) * ds.abs())
+        dq = ds @ k[:i + 1] * c
+        ref.check(dx[i, :hd], dq, eds @ k[:i + 1].abs() * c + r * dq.abs() + 1e-30, "dq")
+    # the last key meets the last query alone
+    p = torch.exp(q[-1] @ k[-1] * c - L)
+    dv = p * dout[-1].double()
+    ref.check(dx[-1, 2 * hd:], dv, (2 * es + 2 * r + (i + 20) * u) * dv.abs() + 1e-30, "dv")
+
+
+def test_gradient_at_the_longest_weights_underflow():
+    """Scores so far apart that all weights but one underflow: the gradient of
+    q and k is zero but for roundings, v's is dout's rows."""
+    import scratch_llama_decoder_b200 as P
+    for dtype in DTYPES:
+        for hd in (32, 64, 128):
+            n = 200
+            qkv = torch.zeros(n, 3 * hd, dtype=dtype, device="cuda")
+            qkv[:, 0] = 64.0
+            qkv[:, hd] = torch.arange(n, device="cuda").to(dtype)  # the row's own key wins
+            qkv[:, 2 * hd:] = torch.randn(n, hd, device="cuda").to(dtype)
+            dout = torch.randn(n, hd, device="cuda").to(dtype)
+            cut = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+            out, lse = P.attention_packed(qkv, cut, 1, 1)
+            dx = P.attention_packed_backward(qkv, cut, 1, 1, out, lse, dout)
+            ro, rl, bo, bl = ref.attention(qkv, [0, n], 1, 1, dtype)
+            ref.check(out, ro, bo, "out")
+            rx, bx = ref.backward(qkv, [0, n], 1, 1, out, lse, dout, dtype)
+            ref.check(dx, rx, bx, "dqkv")

@@ -425,3 +425,159 @@ def test_refused_arguments():
         P.kv_read(pages, table, cu, 1, torch.float16, scales=scales)
     with pytest.raises(ValueError):
         P.kv_pages(4, 16, 2, 64, "int4")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_bad_pages_of_split_sequences(dtype, fmt):
+    """Tables long enough for the split form: bad lengths, bad pages, none."""
+    import scratch_llama_decoder_b200 as P
+    h, g, hd, ps = 8, 2, 64, 16
+    pages, scales = _filled(fmt, 70, ps, g, hd, 20)
+    q = torch.randn(6, h * hd, device="cuda").to(dtype)
+    table = torch.randint(0, 70, (6, 60), generator=torch.Generator().manual_seed(21))
+    table[0, 5], table[0, 40], table[1, 0], table[2, :] = -1, 70, 1 << 30, -(1 << 31)
+    table = table.to(torch.int32).cuda()
+    lens = [960, 200, 900, (1 << 31) - 1, -(1 << 31), 0]
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = P.attention_paged(q, pages, table, lt, scales=scales, flag=flag)
+    assert int(flag) == 2
+    ro, rl, bo, bl = ref.paged(q, pages, scales, table, lens, h, dtype)
+    ref.check(out, ro, bo, "out")
+    live = torch.tensor([True, True, False, True, False, False], device="cuda")
+    ref.check(lse[live], rl[live], bl[live], "lse")
+    assert bool((out[~live] == 0).all() and (lse[~live] == -math.inf).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd,h,g", [(64, 4, 2), (128, 20, 2)])
+def test_most_sequences(hd, h, g, dtype, fmt):
+    """8192 sequences, some long, in pages that all of them share."""
+    import scratch_llama_decoder_b200 as P
+    n, ps, n_pages = 8192, 16, 300
+    pages, scales = _filled(fmt, n_pages, ps, g, hd, 22)
+    gen = torch.Generator().manual_seed(23)
+    lens = torch.randint(0, 40, (n,), generator=gen)
+    some = torch.randperm(n, generator=gen)[:24]
+    lens[some[:12]] = torch.randint(0, 961, (12,), generator=gen)
+    lens[0], lens[-1] = 960, 0
+    table = torch.randint(0, n_pages, (n, 60), generator=gen).to(torch.int32)
+    q = torch.randn(n, h * hd, device="cuda").to(dtype)
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = P.attention_paged(q, pages, table.cuda(), lens.to(torch.int32).cuda(),
+                                 scales=scales, flag=flag)
+    assert int(flag) == 0
+    some = torch.cat([some, torch.tensor([0, 1, n - 2, n - 1])])
+    sl = lens[some].tolist()
+    ro, rl, bo, bl = ref.paged(q[some.cuda()], pages, scales, table[some], sl, h, dtype)
+    live = torch.tensor([x > 0 for x in sl], device="cuda")
+    ref.check(out[some.cuda()], ro, bo, "out")
+    ref.check(lse[some.cuda()][live], rl[live], bl[live], "lse")
+    empty = (lens == 0).cuda()
+    assert bool((out[empty] == 0).all() and (lse[empty] == -math.inf).all())
+    assert bool(torch.isfinite(lse[~empty]).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("long", [False, True])
+def test_a_nan_row_stays_with_its_readers(long, dtype, fmt):
+    """A cached row that is not finite makes the outputs of the sequences and
+    heads that read it NaN, and changes no other's bits; a prefix shared by
+    sequences reads as if each had its own."""
+    import scratch_llama_decoder_b200 as P
+    h, g, hd, ps = 8, 2, 64, 16
+    pages, scales = _filled(fmt, 90, ps, g, hd, 24)
+    cols = 40 if long else 6
+    table = torch.arange(80, dtype=torch.int32).view(2, 40)[:, :cols].repeat(2, 1)
+    table[2:, :2] = table[:1, :2]  # sequences 2 and 3 share the first pages of 0
+    table = table.cuda()
+    lens = [cols * ps, cols * ps - 3, 31, cols * ps]
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(4, h * hd, device="cuda").to(dtype)
+    want = P.attention_paged(q, pages, table, lt, scales=scales)
+    ro, rl, bo, bl = ref.paged(q, pages, scales, table, lens, h, dtype)
+    ref.check(want[0], ro, bo, "out")
+    row = pages[1, :, 1, 3]  # position 19 of sequences 0, 2, 3, kv head 1
+    if scales is None:
+        row[0, 5] = math.nan
+    else:
+        scales[1, 0, 1, 3] = math.nan
+    out, lse = P.attention_paged(q, pages, table, lt, scales=scales)
+    o, w = (t.view(4, g, -1) for t in (out, want[0]))
+    l, wl = (t.view(4, g, -1) for t in (lse, want[1]))
+    for s in range(4):
+        for i in range(g):
+            if i == 1 and s != 1:
+                assert bool(torch.isnan(o[s, i]).all() and torch.isnan(l[s, i]).all())
+            else:
+                assert torch.equal(o[s, i], w[s, i]) and torch.equal(l[s, i], wl[s, i])
+
+
+def test_captured_steps_write_and_attend():
+    """One captured step (write the new tokens, attend, move on) replayed: the
+    positions advance on the device; two streams at once on their own caches."""
+    import scratch_llama_decoder_b200 as P
+    h, g, hd, ps, steps = 8, 2, 64, 16, 40
+    runs = []
+    side = torch.cuda.Stream()
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    for seed in (25, 26):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        pages, scales = P.kv_pages(130, ps, g, hd, "e4m3")
+        table = _tables([40, 40, 40], 130, seed)
+        first = torch.tensor([0, 15, 590], dtype=torch.int32, device="cuda")
+        rows = torch.randn(steps, 3, (h + 2 * g) * hd, generator=gen, device="cuda")
+        rows = rows.to(torch.bfloat16)
+        pos, x = first.clone(), rows[0].clone()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                P.kv_write(x, cu, h, pages, table, scales=scales, starts=pos)
+                pos.add_(1)
+                out, lse = P.attention_paged(x[:, :h * hd], pages, table, pos, scales=scales)
+                k, v = P.kv_read(pages, table, cu, 3, torch.float32, scales=scales, starts=pos - 1)
+        runs.append((pages, scales, table, first, rows, pos, x, graph, out, lse, k, v,
+                     torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for t in range(steps):
+        for _, _, _, _, rows, _, x, graph, out, lse, k, v, st, got in runs:
+            with torch.cuda.stream(st):
+                x.copy_(rows[t])
+                graph.replay()
+                got.append([y.clone() for y in (out, lse, k, v)])
+    torch.cuda.synchronize()
+    for pages, scales, table, first, rows, pos, _, _, _, _, _, _, _, got in runs:
+        assert torch.equal(pos, first + steps)
+        p2, s2 = P.kv_pages(130, ps, g, hd, "e4m3")
+        for t in range(steps):
+            P.kv_write(rows[t], cu, h, p2, table, scales=s2, starts=first + t)
+            o, l = P.attention_paged(rows[t][:, :h * hd], p2, table, first + t + 1, scales=s2)
+            k, v = P.kv_read(p2, table, cu, 3, torch.float32, scales=s2, starts=first + t)
+            for a, b in zip(got[t], (o, l, k, v)):
+                assert torch.equal(a, b)
+        assert torch.equal(p2.view(torch.uint8), pages.view(torch.uint8))
+        assert torch.equal(s2, scales)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_offsets_that_decrease_write_inside_the_cache(dtype):
+    """cu_seqlens of any contents: rows go to places of the tables or nowhere."""
+    import scratch_llama_decoder_b200 as P
+    h, g, hd, ps, n = 4, 2, 32, 8, 100
+    qkv = torch.randn(n, (h + 2 * g) * hd, device="cuda").to(dtype)
+    for cu in ([0, 60, 20, 100], [-50, 1 << 30, 5, -1], [100, 100, 0, 0],
+               [(1 << 31) - 1, -(1 << 31), (1 << 31) - 1, 7]):
+        for fmt in FORMATS:
+            store, scales = _filled(fmt, 12, ps, g, hd, 27)
+            before = store.clone()
+            table = torch.tensor([[0, 1], [2, 3], [4, 5]], dtype=torch.int32, device="cuda")
+            sc = None if scales is None else scales[3:9]
+            cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            P.kv_write(qkv, cut, h, store[3:9], table, scales=sc)
+            k, v = P.kv_read(store[3:9], table, cut, n, dtype, scales=sc)
+            for part in (slice(0, 3), slice(9, 12)):
+                assert torch.equal(store[part].view(torch.uint8), before[part].view(torch.uint8))
