@@ -145,10 +145,12 @@ void packed_plan(const PkArgs &a, const PkPlan &p);
 bool packed_fwd_tc(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *flag);
 bool packed_bwd_tc(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
                    const void *dout, void *dqkv, int64_t dld, int *flag);
-// mma.sync kernels (with their plan): the backward of bfloat16 head sizes to
-// 128, as above.
+// mma.sync kernels (with their plan): bfloat16, head sizes that are multiples
+// of 8 to 128, input rows that start on 16 bytes; false otherwise, and (fwd;
+// bwd where `shorts`) where the sequences are too long for them to win.
+bool packed_fwd_mma(const PkArgs &a, const PkPlan &p, void *o, float *lse);
 bool packed_bwd_mma(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,
-                    const void *dout, void *dqkv, int64_t dld);
+                    const void *dout, void *dqkv, int64_t dld, bool shorts);
 // CUDA-core kernels (with their plan): float32 arithmetic, either type, head sizes to 128.
 bool packed_fwd_tile(const PkArgs &a, const PkPlan &p, void *o, float *lse);
 bool packed_bwd_tile(const PkArgs &a, const PkPlan &p, const void *o, const float *lse,

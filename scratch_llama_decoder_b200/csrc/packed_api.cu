@@ -88,7 +88,8 @@ int llm_kernel_attention_packed_fwd(const void *d_qkv, int64_t ld, int dtype, co
   if (!claim_device(nullptr)) return LLM_ERR_ARG;  // one device per process
   g_launches = 0;
   int *flag = d_flag ? d_flag : p.n_tiles + 1;
-  if (!packed_fwd_tc(a, p, d_o, d_lse, flag) && !packed_fwd_tile(a, p, d_o, d_lse))
+  if (!packed_fwd_mma(a, p, d_o, d_lse) && !packed_fwd_tc(a, p, d_o, d_lse, flag) &&
+      !packed_fwd_tile(a, p, d_o, d_lse))
     return LLM_ERR_CUDA;
   return launched();
 }
@@ -113,8 +114,9 @@ int llm_kernel_attention_packed_bwd(const void *d_qkv, int64_t ld, int dtype, co
   if (!claim_device(nullptr)) return LLM_ERR_ARG;
   g_launches = 0;
   int *flag = d_flag ? d_flag : p.n_tiles + 1;
-  if (!packed_bwd_tc(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld, flag) &&
-      !packed_bwd_mma(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld) &&
+  if (!packed_bwd_mma(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld, true) &&
+      !packed_bwd_tc(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld, flag) &&
+      !packed_bwd_mma(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld, false) &&
       !packed_bwd_tile(a, p, d_o, d_lse, d_dout, d_dqkv, dqkv_ld))
     return LLM_ERR_CUDA;
   return launched();

@@ -481,3 +481,28 @@ def test_gradient_at_the_longest_weights_underflow():
             ref.check(out, ro, bo, "out")
             rx, bx = ref.backward(qkv, [0, n], 1, 1, out, lse, dout, dtype)
             ref.check(dx, rx, bx, "dqkv")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_many_long_sequences(hd, dtype):
+    """Hundreds of sequences of several tiles: the same bits as in calls of a
+    few sequences each; and shorter ones, against the formulas."""
+    import scratch_llama_decoder_b200 as P
+    h, g, count = 2, 2, 300
+    gen = torch.Generator().manual_seed(20)
+    lens = torch.randint(300, 700, (count,), generator=gen).tolist()
+    qkv, dout, cu, cut = _data(lens, h, g, hd, dtype, seed=20)
+    out, lse = P.attention_packed(qkv, cut, h, g)
+    dx = P.attention_packed_backward(qkv, cut, h, g, out, lse, dout)
+    for s in (0, 100, 296):
+        a, b = cu[s], cu[s + 4]
+        part = cut[s:s + 5] - a
+        o, l = P.attention_packed(qkv[a:b].contiguous(), part, h, g)
+        d = P.attention_packed_backward(qkv[a:b].contiguous(), part, h, g, o, l, dout[a:b])
+        assert torch.equal(o, out[a:b]) and torch.equal(l, lse[:, a:b])
+        assert torch.equal(d, dx[a:b])
+    lens = torch.randint(1, 300, (40,), generator=gen).tolist()
+    for h, g in ((8, 8), (4, 2)):
+        qkv, dout, cu, cut = _data(lens, h, g, hd, dtype, seed=21)
+        _check(qkv, dout, cu, cut, h, g)
