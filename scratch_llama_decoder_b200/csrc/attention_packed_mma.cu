@@ -21,15 +21,15 @@
 // backward) however few rows it has.  These have 3 to 5 blocks of 64 rows, at a
 // third of the rate.  So they win where sequences are short, by the mean of
 // n_rows / n_seq (16384 rows, 8 heads, us, these and tcgen05's):
-//   forward   heads of 32: 64 rows 18.5, 33; 192: 17.9, 23.2; 256: 18.5, 17.9
-//             64: 64 rows 23.8, 33; 80: 30.0, 27.6   128: 64: 38, 42; 96: 45, 31
-//             one wave of blocks (4 sequences), heads of 64: 128: 3.7, 4.7; 256:
-//             6.5, 5.7; of 128: 128: 5.4, 5.2
-//   backward  heads of 32: 64 rows 32, 107; 256: 41, 52; 320: 45, 70; 512: 59, 60
-//             (2 kv heads 320: 54, 63; 384: 59, 50); 64: 64 rows 50, 111; 192: 64,
-//             76; 256: 71, 56 (2 kv heads 128: 50, 44)
-//             few blocks: 16 sequences, 2 kv heads of 32: 128: 14, 15; 256: 24, 22;
-//             of 64: 64: 15, 16; 100: 25, 16
+//   forward   heads of 32: 64 rows 28, 50; 192: 27, 35; 256: 28, 27
+//             64: 64 rows 36, 50; 80: 45, 41   128: 64: 57, 63; 96: 67, 47
+//             one wave of blocks (4 sequences), heads of 64: 128: 5.6, 7.0; 256:
+//             9.8, 8.6; of 128: 128: 8.1, 7.8
+//   backward  heads of 32: 64 rows 48, 160; 256: 61, 78; 320: 68, 105; 512: 89, 90
+//             (2 kv heads 320: 80, 94; 384: 89, 75); 64: 64 rows 76, 166; 192: 95,
+//             114; 256: 106, 84 (2 kv heads 128: 74, 66)
+//             few blocks: 16 sequences, 2 kv heads of 32: 128: 21, 23; 256: 35, 33;
+//             of 64: 64: 22, 23; 100: 38, 24
 #include "packed.cuh"
 #include "tcgen05.cuh"
 

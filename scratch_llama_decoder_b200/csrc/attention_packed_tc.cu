@@ -395,8 +395,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int c = 0; c < 2; c++) {
           uint32_t pw[32];
           if (diag) {  // on the SFU alone: masked scores give exact zeros
-            weights<false>(sv + 64 * c, sl2, mr, pw, l2);
-            weights<false>(sv + 64 * c + 32, sl2, mr, pw + 16, l2);
+#pragma unroll
+            for (int d = 0; d < 2; d++) {
+              if (2 * c + d <= quarter) {
+                weights<false>(sv + 64 * c + 32 * d, sl2, mr, pw + 16 * d, l2);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; i++) pw[16 * d + i] = 0;
+              }
+            }
           } else {
             weights<true>(sv + 64 * c, sl2, mr, pw, l2);
             weights<true>(sv + 64 * c + 32, sl2, mr, pw + 16, l2);

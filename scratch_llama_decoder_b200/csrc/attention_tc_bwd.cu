@@ -78,8 +78,9 @@ constexpr float LOG2E = 1.4426950408889634f;
 // barriers | red[2] | -L
 constexpr int DQ_COL_S = 0, DQ_COL_DP = 128, DQ_COL_DS = 256, DQ_COL_DQA = 320, DQ_COL_DQB = 384;
 constexpr int BAR_BYTES = 512;  // 48 mbarrier slots, then the TMEM address and abort words
+constexpr int RED = 2 * NCQ * 128;  // floats of one exchange of the row groups
 constexpr int DQ_SMEM =
-    (5 + 2 * STAGES) * TILE_BYTES + 1024 + BAR_BYTES + 2 * NCQ * 128 * 4 + 128 * 4;
+    (5 + 2 * STAGES) * TILE_BYTES + 1024 + BAR_BYTES + 2 * RED * 4 + 128 * 4;
 // dK/dV kernel: TMEM columns; shared memory K[2] | V[2] | Q[STAGES] | dO[STAGES] |
 // L[STAGES] | D[STAGES] | barriers
 constexpr int KV_COL_S = 0, KV_COL_DP = 128, KV_COL_P = 256, KV_COL_DS = 320, KV_COL_DV = 384,
@@ -162,8 +163,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t *bars = (uint64_t *)(sV + STAGES * TILE_BYTES);
   uint32_t *tmem_sh = (uint32_t *)(bars + 48);
   volatile int *abort_sh = (volatile int *)(tmem_sh + 1);
-  float *red = (float *)(bars + BAR_BYTES / 8);  // [2][NCQ][128] partial dot products
-  float *sNL = red + 2 * NCQ * 128;              // [128] L of the item's rows (rows < T)
+  float *red = (float *)(bars + BAR_BYTES / 8);  // [2][2][NCQ][128] parts of row sums
+  float *sNL = red + 2 * RED;                    // [128] L of the item's rows (rows < T)
   const uint32_t b0 = smem_u32(bars);
   const uint32_t qd_full = b0, qd_empty = b0 + 16,  // [2]: Q/dO slot
                  o_full = b0 + 32, o_empty = b0 + 40, k_full = b0 + 48,
@@ -453,17 +454,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float nl2 = valid ? -sNL[r] * LOG2E : -INFINITY;
       mbar_arrive(o_empty);              // this thread's O row and -L consumed
       mbar_arrive(qd_empty + 8 * slot);  // and its dO row
-      // sum of v over the row's four column groups, the four warps of this lane
-      // quarter (false: a wait gave up)
-      auto row_sum = [&](float v, float &sum) {
-        float *rd = red + (qr & 1) * NCQ * 128;
+      // sums of v and w over the row's four column groups, the four warps of this
+      // lane quarter (false: a wait gave up); w only where two are wanted
+      auto row_sums = [&](float &v, float &w, bool two) {
+        float *rd = red + (qr & 1) * RED, *rw = rd + NCQ * 128;
         rd[cq * 128 + r] = v;
+        if (two) rw[cq * 128 + r] = w;
         mbar_arrive(qred + 8 * quarter);
         if (!warp_wait(qred + 8 * quarter, qr & 1, abort_sh, gflag)) return false;
         qr++;
-        sum = 0.f;
+        v = 0.f;
 #pragma unroll
-        for (int c = 0; c < NCQ; c++) sum += rd[c * 128 + r];
+        for (int c = 0; c < NCQ; c++) v += rd[c * 128 + r];
+        if (two) {
+          w = 0.f;
+#pragma unroll
+          for (int c = 0; c < NCQ; c++) w += rw[c * 128 + r];
+        }
         return true;
       };
       // Packed, a sequence's first 128 rows: D = sum_j P_ij dP_ij / sum_j P_ij of
@@ -471,8 +478,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // cancel where dP is the same for all).  dO . O takes O as it was rounded
       // to bf16, and where O has few terms that error is as large as dS's own.
       const bool own_d = PK && nj == 1;
-      float Di = 0.f;
-      if (!own_d && !row_sum(dpart, Di)) {
+      float Di = dpart, unused = 0.f;
+      if (!own_d && !row_sums(Di, unused, false)) {
         ok = false;
         break;
       }
@@ -505,41 +512,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int k0 = j * BK + cq * CW;
         const bool diag = (j == qb);  // only the diagonal block masks (keys >= T lie above it)
         uint32_t w[CW / 2];
-        if (PK && own_d) {
-          float part = 0.f, l = 0.f;
+        if (diag) {  // the causal mask only on the diagonal block
 #pragma unroll
           for (int i = 0; i < CW; i += 2) {
             const float2 p = exp2_split<NP_DQ>(
                 __ffma2_rn(make_float2(sv[i], sv[i + 1]), make_float2(sl2, sl2), nl), i / 2);
-            if (k0 + i <= qi) {
-              part += p.x * dv[i];
-              l += p.x;
-            }
-            if (k0 + i + 1 <= qi) {
-              part += p.y * dv[i + 1];
-              l += p.y;
+            sv[i] = k0 + i > qi ? 0.f : p.x;
+            sv[i + 1] = k0 + i + 1 > qi ? 0.f : p.y;
+            if constexpr (PK) {  // dP of a key past the sequence may be no number
+              if (k0 + i > qi) dv[i] = 0.f;
+              if (k0 + i + 1 > qi) dv[i + 1] = 0.f;
             }
           }
-          if (!row_sum(part, Di) || !row_sum(l, part)) {
-            ok = false;
-            break;
+          if (PK && own_d) {
+            float l = 0.f;
+            Di = 0.f;
+#pragma unroll
+            for (int i = 0; i < CW; i++) {
+              Di += sv[i] * dv[i];
+              l += sv[i];
+            }
+            if (!row_sums(Di, l, true)) {
+              ok = false;
+              break;
+            }
+            Di /= l;
+            if (cq == 0 && valid) Dv[di] = Di;
+            nd = make_float2(-Di, -Di);
           }
-          Di /= part;
-          if (cq == 0 && valid) Dv[di] = Di;
-          nd = make_float2(-Di, -Di);
-        }
-        if (diag) {  // the causal mask only on the diagonal block
 #pragma unroll
           for (int i = 0; i < CW; i += 2) {
-            float2 p = exp2_split<NP_DQ>(
-                __ffma2_rn(make_float2(sv[i], sv[i + 1]), make_float2(sl2, sl2), nl), i / 2);
-            if (k0 + i > qi) p.x = 0.f;
-            if (k0 + i + 1 > qi) p.y = 0.f;
-            float2 ds = __fmul2_rn(p, __fadd2_rn(make_float2(dv[i], dv[i + 1]), nd));
-            if constexpr (PK) {  // dP of a key past the sequence may be no number
-              if (k0 + i > qi) ds.x = 0.f;
-              if (k0 + i + 1 > qi) ds.y = 0.f;
-            }
+            const float2 ds = __fmul2_rn(make_float2(sv[i], sv[i + 1]),
+                                         __fadd2_rn(make_float2(dv[i], dv[i + 1]), nd));
             w[i / 2] = pack_bf16(ds.x, ds.y);
           }
         } else {
