@@ -256,8 +256,8 @@ LLM_DEV void tiles_ready() {
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 }
-// s[r][c] = A[R ty + r] . B[tx + 16 c]
-template <int HD, int R>
+// s[r][c] = A[R ty + r] . B[tx + 16 c] for c in [C0, C1), 0 for the others.
+template <int HD, int R, int C0 = 0, int C1 = 4>
 LLM_DEV void dot(const float *A, const float *B, int tx, int ty, float (&s)[R][4]) {
   float2 acc[R][4];
 #pragma unroll
@@ -268,13 +268,13 @@ LLM_DEV void dot(const float *A, const float *B, int tx, int ty, float (&s)[R][4
   for (int e = 0; e < HD; e += 4) {
     float4 b[4];
 #pragma unroll
-    for (int c = 0; c < 4; c++)
+    for (int c = C0; c < C1; c++)
       b[c] = *reinterpret_cast<const float4 *>(B + (tx + 16 * c) * (HD + 4) + e);
 #pragma unroll
     for (int r = 0; r < R; r++) {
       const float4 a = *reinterpret_cast<const float4 *>(A + (R * ty + r) * (HD + 4) + e);
 #pragma unroll
-      for (int c = 0; c < 4; c++) {
+      for (int c = C0; c < C1; c++) {
         acc[r][c] = __ffma2_rn(make_float2(a.x, a.y), make_float2(b[c].x, b[c].y), acc[r][c]);
         acc[r][c] = __ffma2_rn(make_float2(a.z, a.w), make_float2(b[c].z, b[c].w), acc[r][c]);
       }
@@ -285,6 +285,12 @@ LLM_DEV void dot(const float *A, const float *B, int tx, int ty, float (&s)[R][4
 #pragma unroll
     for (int c = 0; c < 4; c++) s[r][c] = acc[r][c].x + acc[r][c].y;
 }
+// The warp's number within the block's rows: turned by the block, so that the
+// warps with the most work of a diagonal tile do not all fall on one scheduler.
+template <int HD>
+LLM_DEV int row_warp() {
+  return ((threadIdx.x >> 5) + (blockIdx.x >> 1)) & (threads_of<HD>() / 32 - 1);
+}
 template <int R>
 LLM_DEV void put(float *P, const float (&p)[R][4], int tx, int ty) {
 #pragma unroll
@@ -292,11 +298,12 @@ LLM_DEV void put(float *P, const float (&p)[R][4], int tx, int ty) {
 #pragma unroll
     for (int c = 0; c < 4; c++) P[(R * ty + r) * LDP + ((tx + 16 * c) ^ ((ty & 1) * 16))] = p[r][c];
 }
-// out[r][c] += sum_k P[R ty + r][k] M[k][out_col(c)]
+// out[r][c] += sum_k P[R ty + r][k] M[k][out_col(c)] over k in [k0, k1), multiples of 8
 template <int HD, int R>
-LLM_DEV void accumulate(const float *P, const float *M, int tx, int ty, float (&out)[R][HD / 16]) {
+LLM_DEV void accumulate(const float *P, const float *M, int tx, int ty, float (&out)[R][HD / 16],
+                        int k0, int k1) {
 #pragma unroll 2
-  for (int k = 0; k < TB; k += 4) {
+  for (int k = k0; k < k1; k += 4) {
     float4 p[R];
 #pragma unroll
     for (int r = 0; r < R; r++)
@@ -357,11 +364,13 @@ __global__ void __launch_bounds__(threads_of<HD>())
   if (!pk_item64(tl, H, t, h, half)) return;
   const int q0 = t.blk * PK_BLOCK + half * TB;
   if (q0 >= t.len) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, g = h / (H / Hkv);
+  const int wr = row_warp<HD>(), tx = threadIdx.x & 15, ty = 2 * wr + (threadIdx.x >> 4 & 1);
+  const int g = h / (H / Hkv), w0 = 2 * R * wr;  // the warp's first row: it has 2 R
   const float sl2 = LOG2E / sqrtf((float)hd);
   const T *base = qkv + (int64_t)t.row0 * ld;
   const T *kcol = base + (int64_t)(H + g) * hd, *vcol = base + (int64_t)(H + Hkv + g) * hd;
-  load_tile<T, HD>(Q, base + q0 * ld + (int64_t)h * hd, ld, min(TB, t.len - q0), hd, vec);
+  const int nq = min(TB, t.len - q0);
+  load_tile<T, HD>(Q, base + q0 * ld + (int64_t)h * hd, ld, nq, hd, vec);
   float m[R], l[R], acc[R][HD / 16];
 #pragma unroll
   for (int r = 0; r < R; r++) {
@@ -371,19 +380,23 @@ __global__ void __launch_bounds__(threads_of<HD>())
     for (int c = 0; c < HD / 16; c++) acc[r][c] = 0.f;
   }
   for (int k0 = 0; k0 <= q0; k0 += TB) {
-    __syncthreads();  // the previous tile's products are done with K, V and P
+    __syncthreads();  // the previous tile's products are done with K and V
     const int nk = min(TB, t.len - k0);
     load_tile<T, HD>(K, kcol + k0 * ld, ld, nk, hd, vec);
     load_tile<T, HD>(V, vcol + k0 * ld, ld, nk, hd, vec);
     tiles_ready();
+    if (w0 >= nq) continue;  // no row of the sequence
+    // up to the warp's last row
+    const bool diag = k0 == q0;
     float s[R][4];
-    dot<HD, R>(Q, K, tx, ty, s);
+    if (diag && w0 + 2 * R <= TB / 2) dot<HD, R, 0, 2>(Q, K, tx, ty, s);
+    else dot<HD, R>(Q, K, tx, ty, s);
 #pragma unroll
     for (int r = 0; r < R; r++) {
 #pragma unroll
       for (int c = 0; c < 4; c++) {
         s[r][c] *= sl2;
-        if (k0 == q0 && tx + 16 * c > R * ty + r) s[r][c] = -INFINITY;
+        if (diag && tx + 16 * c > R * ty + r) s[r][c] = -INFINITY;
       }
       const float mn =
           fmaxf(m[r], half_max(fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]))));
@@ -396,9 +409,10 @@ __global__ void __launch_bounds__(threads_of<HD>())
 #pragma unroll
       for (int c = 0; c < HD / 16; c++) acc[r][c] *= corr;
     }
+    __syncwarp();  // P's rows are the warp's own
     put<R>(P, s, tx, ty);
-    __syncthreads();
-    accumulate<HD, R>(P, V, tx, ty, acc);
+    __syncwarp();
+    accumulate<HD, R>(P, V, tx, ty, acc, 0, diag ? w0 + 2 * R : TB);
   }
 #pragma unroll
   for (int r = 0; r < R; r++) {
@@ -427,7 +441,8 @@ __global__ void __launch_bounds__(threads_of<HD>())
   if (!pk_item64(tl, H, t, h, half)) return;
   const int q0 = t.blk * PK_BLOCK + half * TB;
   if (q0 >= t.len) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, g = h / (H / Hkv);
+  const int wr = row_warp<HD>(), tx = threadIdx.x & 15, ty = 2 * wr + (threadIdx.x >> 4 & 1);
+  const int g = h / (H / Hkv), w0 = 2 * R * wr;  // the warp's first row: it has 2 R
   const int nq = min(TB, t.len - q0);
   const int64_t ow = (int64_t)H * hd;
   const float scale = 1.0f / sqrtf((float)hd), sl2 = scale * LOG2E;
@@ -460,20 +475,28 @@ __global__ void __launch_bounds__(threads_of<HD>())
     load_tile<T, HD>(K, kcol + k0 * ld, ld, nk, hd, vec);
     load_tile<T, HD>(V, vcol + k0 * ld, ld, nk, hd, vec);
     tiles_ready();
+    if (w0 >= nq) continue;  // no row of the sequence
+    const bool diag = k0 == q0;  // up to the warp's last row
     float s[R][4], dp[R][4];
-    dot<HD, R>(Q, K, tx, ty, s);
-    dot<HD, R>(G, V, tx, ty, dp);
+    if (diag && w0 + 2 * R <= TB / 2) {
+      dot<HD, R, 0, 2>(Q, K, tx, ty, s);
+      dot<HD, R, 0, 2>(G, V, tx, ty, dp);
+    } else {
+      dot<HD, R>(Q, K, tx, ty, s);
+      dot<HD, R>(G, V, tx, ty, dp);
+    }
 #pragma unroll
     for (int r = 0; r < R; r++)
 #pragma unroll
       for (int c = 0; c < 4; c++) {
-        const bool masked = k0 == q0 && tx + 16 * c > R * ty + r;
+        const bool masked = diag && tx + 16 * c > R * ty + r;
         const float p = ex2(s[r][c] * sl2 - Lr[r]);
         s[r][c] = masked ? 0.f : p * (dp[r][c] - Dr[r]);
       }
+    __syncwarp();  // S's rows are the warp's own
     put<R>(S, s, tx, ty);
-    __syncthreads();
-    accumulate<HD, R>(S, K, tx, ty, dq);
+    __syncwarp();
+    accumulate<HD, R>(S, K, tx, ty, dq, 0, diag ? w0 + 2 * R : TB);
   }
 #pragma unroll
   for (int r = 0; r < R; r++)
@@ -500,7 +523,8 @@ __global__ void __launch_bounds__(threads_of<HD>())
   const int n = (t.len + PK_BLOCK - 1) / PK_BLOCK;
   const int k0 = (n - 1 - t.blk) * PK_BLOCK + half * TB;
   if (k0 >= t.len) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, grp = H / Hkv;
+  const int wr = row_warp<HD>(), tx = threadIdx.x & 15, ty = 2 * wr + (threadIdx.x >> 4 & 1);
+  const int grp = H / Hkv, w0 = 2 * R * wr;  // the warp's first row: it has 2 R
   const int nk = min(TB, t.len - k0);
   const int64_t ow = (int64_t)H * hd;
   const float scale = 1.0f / sqrtf((float)hd), sl2 = scale * LOG2E;
@@ -526,27 +550,35 @@ __global__ void __launch_bounds__(threads_of<HD>())
         sD[threadIdx.x] = in ? ld_float(D + li) : 0.f;
       }
       tiles_ready();
-      float s[R][4], dp[R][4];
-      dot<HD, R>(K, Q, tx, ty, s);  // rows keys, columns queries
-      dot<HD, R>(V, G, tx, ty, dp);
+      if (w0 >= nk) continue;  // no key of the sequence
+      const bool diag = q0 == k0;  // from the warp's first key on
+      float s[R][4], dp[R][4];  // rows keys, columns queries
+      if (diag && w0 >= TB / 2) {
+        dot<HD, R, 2, 4>(K, Q, tx, ty, s);
+        dot<HD, R, 2, 4>(V, G, tx, ty, dp);
+      } else {
+        dot<HD, R>(K, Q, tx, ty, s);
+        dot<HD, R>(V, G, tx, ty, dp);
+      }
 #pragma unroll
       for (int c = 0; c < 4; c++) {
         const float L = sL[tx + 16 * c], d = sD[tx + 16 * c];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-          const bool masked = q0 == k0 && R * ty + r > tx + 16 * c;
+          const bool masked = diag && R * ty + r > tx + 16 * c;
           const float e = masked ? 0.f : ex2(s[r][c] * sl2 - L);
           s[r][c] = e;
           dp[r][c] = masked ? 0.f : e * (dp[r][c] - d);
         }
       }
+      __syncwarp();  // P's rows are the warp's own
       put<R>(P, s, tx, ty);
-      __syncthreads();
-      accumulate<HD, R>(P, G, tx, ty, dv);
-      __syncthreads();  // one tile holds P, then dS
+      __syncwarp();
+      accumulate<HD, R>(P, G, tx, ty, dv, diag ? w0 : 0, TB);
+      __syncwarp();  // one tile holds P, then dS
       put<R>(P, dp, tx, ty);
-      __syncthreads();
-      accumulate<HD, R>(P, Q, tx, ty, dk);
+      __syncwarp();
+      accumulate<HD, R>(P, Q, tx, ty, dk, diag ? w0 : 0, TB);
     }
   }
 #pragma unroll
