@@ -964,7 +964,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const float2 x23 = __ffma2_rn(make_float2(sv[i + 2], sv[i + 3]),
                                           make_float2(sl2, sl2), nl23);
             float2 p01 = exp2_split<NP_DKV>(x01, c / 2), p23 = exp2_split<NP_DKV>(x23, c / 2 + 1);
-            if (diag) {
+            if (!PK && diag) {
               if (kj > qc0 + c) p01.x = 0.f;
               if (kj > qc0 + c + 1) p01.y = 0.f;
               if (kj > qc0 + c + 2) p23.x = 0.f;
@@ -980,14 +980,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             wd[i / 2 + 1] = pack_bf16(d23.x, d23.y);
           }
           if constexpr (PK) {
-            // queries past the sequence's end, and what the causal mask puts
-            // to 0 beside a dP that may be no number
+            // the causal mask, and queries past the sequence's end, whose dP may
+            // be no number: both set to 0
             if (diag || qc0 + CW > T) {
+              const int lo = kj - qc0 - hf * HC, n = max(T - kj, 0);  // keep [lo, lo + n)
 #pragma unroll
               for (int i = 0; i < HC; i += 2) {
-                const int q = qc0 + hf * HC + i;
-                const uint32_t keep = (q < T && kj <= q ? 0xffffu : 0u) |
-                                      (q + 1 < T && kj <= q + 1 ? 0xffff0000u : 0u);
+                const uint32_t keep = ((uint32_t)(i - lo) < (uint32_t)n ? 0xffffu : 0u) |
+                                      ((uint32_t)(i + 1 - lo) < (uint32_t)n ? 0xffff0000u : 0u);
                 wp[i / 2] &= keep;
                 wd[i / 2] &= keep;
               }
