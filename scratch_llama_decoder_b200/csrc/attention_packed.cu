@@ -196,7 +196,10 @@ __global__ void __launch_bounds__(FEW) k_plan_few(const int32_t *__restrict__ cu
 // with bit 4 turned (both ty of a warp would store to the same banks).  Head
 // columns past hd are zero, so a head size runs on the next of 32, 64, 128.
 // Against 4 x 4 results a thread from transposed tiles: training step of
-// 16384 rows, 4 heads of 32, 538 -> 400 us.
+// 16384 rows, 4 heads of 32, 538 -> 397 us (4 sequences of 2048 rows: forward 27,
+// backward 22 TFLOP/s of the 74 of the FMA pipes).  What bounds it is the
+// latency of 8 warps an SM: a thread's results take 173 to 232 registers, and
+// cut to 168 or 128 for 3 or 4 blocks an SM they spill (422 and 557 us).
 constexpr int TB = 64, LDP = TB + 4;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // 2^x, the SFU's instruction alone (relative error 2^-22): exp2f adds the

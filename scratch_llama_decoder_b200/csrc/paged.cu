@@ -96,14 +96,15 @@ template <int FMT>
 LLM_DEV void decode8(const uint32_t (&c)[2], float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    const uint32_t w = c[i >> 2] >> (8 * (i & 3));
     if constexpr (FMT == KV_E4M3) {
-      const float2 v = e4m3x2(w);
+      const float2 v = e4m3x2(c[i >> 2] >> (8 * (i & 3)));
       x[i] = v.x;
       x[i + 1] = v.y;
     } else {
-      x[i] = (float)(int8_t)(w & 0xff);
-      x[i + 1] = (float)(int8_t)(w >> 8 & 0xff);
+      // code + 128 as the low mantissa bits of 2^23 (a conversion runs at the SFU's rate)
+      const uint32_t u = c[i >> 2] ^ 0x80808080u;
+      x[i] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 + (i & 3))) - 8388736.f;
+      x[i + 1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7541 + (i & 3))) - 8388736.f;
     }
   }
 }
@@ -391,14 +392,20 @@ LLM_DEV int seq_at(const int *pre, int n_seq, int64_t w, int Hkv) {
 }
 
 // 4 warps; a warp takes 4 positions at a time, 8 lanes each, a lane HD / 8 of
-// the head's columns, and GT query heads of the kv head at once.
-template <typename T, int FMT, int HD, int GT>
+// the head's columns, and GT query heads of the kv head at once; U such groups
+// of positions have their loads in flight together.  The float32 form, and that
+// of layouts the tensor-core kernel does not take.  32 sequences of 4096
+// positions, 16 heads of 64 (float32 queries): float32 cache 165 us (6.5 TB/s;
+// U = 1: 239), bfloat16 209 (U = 1: 319), 8-bit 257 (U = 4: 394, 1: 337), bound by
+// the arithmetic a position costs (a dot product, 3 shuffles and an exponential
+// for 8 lanes), as are grouped heads.
+template <typename T, int FMT, int HD, int GT, bool VEC>
 __global__ void __launch_bounds__(AT)
     k_attend(const KvView kv, const T *__restrict__ q, int64_t q_ld,
              const int32_t *__restrict__ lens, const Sched sc, int H, T *__restrict__ o,
-             float *__restrict__ lse, int *__restrict__ pre_out, float *__restrict__ part,
-             bool vec) {
+             float *__restrict__ lse, int *__restrict__ pre_out, float *__restrict__ part) {
   constexpr int EPL = HD / 8, NC = (EPL + 7) / 8;  // columns a lane, 8-element pieces
+  constexpr int U = FMT < KV_E4M3 && EPL * GT <= 8 ? 4 : EPL * GT <= 32 ? 2 : 1;
   extern __shared__ int pre[];
   __shared__ float sm[AT / 32][GT][HD + 2];
   pk_release();
@@ -453,51 +460,71 @@ __global__ void __launch_bounds__(AT)
           acc[r][c] = 0.f;
         }
       }
-      for (int j = j0 + warp * 4; j < j1; j += AT / 32 * 4) {
-        const int jj = j + ks;
-        const int64_t row = jj < j1 ? kv_row(kv, s, jj) : -1;
-        if (jj < j1 && row < 0 && kv.flag && sub == 0) atomicOr(kv.flag, PK_BAD_PAGE);
-        const int64_t kr = row + (int64_t)g * kv.ps, vr = kr + (int64_t)kv.Hkv * kv.ps;
-        float kx[8 * NC], vx[8 * NC], vs = 1.f, kscale = 1.f;
+      bool bad = false;  // a position without a place
+      for (int j = j0 + warp * 4; j < j1; j += AT / 32 * 4 * U) {
+        int64_t kr[U], row[U];
+        float kx[U][8 * NC], vx[U][8 * NC], vs[U], kscale[U];
 #pragma unroll
-        for (int c = 0; c < NC; c++) {
-          float a[8] = {}, b[8] = {};
-          const int e = sub * EPL + 8 * c, n = min(hd - e, EPL - 8 * c);
-          if (row >= 0 && n > 0) {
-            kv_read8<FMT>(kv.pages, kr * hd + e, vec && n >= 8, n, a);
-            kv_read8<FMT>(kv.pages, vr * hd + e, vec && n >= 8, n, b);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            kx[8 * c + i] = a[i];
-            vx[8 * c + i] = b[i];
-          }
+        for (int u = 0; u < U; u++) {
+          const int jj = j + u * (AT / 32 * 4) + ks;
+          row[u] = jj < j1 ? kv_row(kv, s, jj) : -1;
+          bad |= jj < j1 && row[u] < 0;
+          kr[u] = row[u] + (int64_t)g * kv.ps;
         }
-        if constexpr (FMT >= KV_E4M3) {
-          if (row >= 0) {
-            kscale = kv.scales[kr];
-            vs = kv.scales[vr];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const int64_t vr = kr[u] + (int64_t)kv.Hkv * kv.ps;
+#pragma unroll
+          for (int c = 0; c < NC; c++) {
+            float a[8] = {}, b[8] = {};
+            const int e = sub * EPL + 8 * c, n = min(hd - e, EPL - 8 * c);
+            if (row[u] >= 0 && n > 0) {
+              kv_read8<FMT>(kv.pages, kr[u] * hd + e, VEC && EPL >= 8, n, a);
+              kv_read8<FMT>(kv.pages, vr * hd + e, VEC && EPL >= 8, n, b);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              kx[u][8 * c + i] = a[i];
+              vx[u][8 * c + i] = b[i];
+            }
+          }
+          vs[u] = kscale[u] = 1.f;
+          if constexpr (FMT >= KV_E4M3) {
+            if (row[u] >= 0) {
+              kscale[u] = kv.scales[kr[u]];
+              vs[u] = kv.scales[vr];
+            }
           }
         }
 #pragma unroll
         for (int r = 0; r < GT; r++) {
-          float t = 0.f;
+          float t[U], mn = m[r];
 #pragma unroll
-          for (int c = 0; c < EPL; c++) t = fmaf(qv[r][c], kx[c], t);
+          for (int u = 0; u < U; u++) {
+            t[u] = 0.f;
 #pragma unroll
-          for (int x = 1; x < 8; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-          t *= kscale;
-          if (row < 0) t = -INFINITY;  // no such position: weight 0, v read as 0
-          const float mn = fmaxf(m[r], t);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          const float corr = exp2f(m[r] - ref), p = exp2f(t - ref);
-          l[r] = l[r] * corr + p;
+            for (int c = 0; c < EPL; c++) t[u] = fmaf(qv[r][c], kx[u][c], t[u]);
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) t[u] += __shfl_xor_sync(0xffffffffu, t[u], x);
+            t[u] *= kscale[u];
+            if (row[u] < 0) t[u] = -INFINITY;  // no such position: weight 0, v read as 0
+            mn = fmaxf(mn, t[u]);
+          }
+          const float ref = mn == -INFINITY ? 0.f : mn, corr = exp2f(m[r] - ref);
+          l[r] *= corr;
           m[r] = mn;
-          const float pv = p * vs;
 #pragma unroll
-          for (int c = 0; c < EPL; c++) acc[r][c] = fmaf(pv, vx[c], acc[r][c] * corr);
+          for (int c = 0; c < EPL; c++) acc[r][c] *= corr;
+#pragma unroll
+          for (int u = 0; u < U; u++) {
+            const float p = exp2f(t[u] - ref), pv = p * vs[u];
+            l[r] += p;
+#pragma unroll
+            for (int c = 0; c < EPL; c++) acc[r][c] = fmaf(pv, vx[u][c], acc[r][c]);
+          }
         }
       }
+      if (bad && kv.flag && sub == 0) atomicOr(kv.flag, PK_BAD_PAGE);
       // the warp's 4 position groups meet, then the 4 warps
 #pragma unroll
       for (int x = 8; x < 32; x <<= 1)
@@ -588,6 +615,10 @@ __global__ void __launch_bounds__(AT)
 // as two bfloat16 terms (2^-17: rounded to one, the outputs of a long context
 // were 1.45 times as far off as their own rounding; the loads hide the second
 // product).
+// Measured: 32 sequences to 16384 positions, 16 heads of 64, e4m3, 280 MB: 55 us,
+// 5.1 TB/s; one of 100001, bfloat16, 410 MB: 72 us, 5.7 TB/s, the loads' latency
+// (10.7 of the 15 cycles between a warp's instructions) at 4 warps a scheduler,
+// which is all that the operands' registers leave room for.
 constexpr int NW = AT / 32;
 // Blocks per SM: what the registers of a lane's operands leave room for.
 constexpr int mma_blocks(int HD, int NT) { return NT == 2 ? 2 : HD == 128 ? 3 : 4; }
@@ -1172,11 +1203,13 @@ static bool attend(const PagedArgs &a, const Sched &sc, int *pre, float *part, b
   auto go = [&](auto kern) {
     if (!smem_optin((const void *)kern, 4 * (PG_MAX_SEQ + 1))) return false;
     kern<<<sc.N, AT, smem, a.s>>>(a.kv, (const T *)a.q, a.q_ld, a.lens, sc, a.H, (T *)a.o, a.lse,
-                                  pre, part, vec);
+                                  pre, part);
     count_launch();
     return true;
   };
-  if (!(grp == 1 ? go(k_attend<T, FMT, HD, 1>) : go(k_attend<T, FMT, HD, 4>))) return false;
+  if (!(grp == 1 ? vec ? go(k_attend<T, FMT, HD, 1, true>) : go(k_attend<T, FMT, HD, 1, false>)
+                 : vec ? go(k_attend<T, FMT, HD, 4, true>) : go(k_attend<T, FMT, HD, 4, false>)))
+    return false;
   if (!sc.direct) {
     join<T>(a, sc, pre, part);
   }
@@ -1240,13 +1273,16 @@ static bool attend_fmt(const PagedArgs &a, const Sched &sc, int *pre, float *par
   }
 }
 
-// Blocks of a call: the machine's worth of blocks, or one per pair when that
-// cannot cut a pair worth the join.
+// Blocks of a call: the machine's worth of blocks, or one per pair where tables
+// are short, which saves the prefix, the second kernel and the workspace (8
+// heads, 2 kv heads of 64, bfloat16, lengths to the table's: 1 sequence of 512
+// at most 4.9 us, split 8.0; of 1024, 10.1 and 7.4; 32 sequences of 1024, 10.4
+// and 12.4, 128: 12.5 and 15.5; of 2048: 17.4 and 13.9, 24.4 and 20.9).
 static Sched schedule(const KvView &kv, int n_seq) {
   Sched sc{n_seq, kv.Hkv, 0, 0};
   const int64_t pairs = (int64_t)n_seq * kv.Hkv;
   const int64_t cap = (int64_t)kv.table_pages * kv.ps;
-  sc.direct = cap <= 8 * PG_UNIT;
+  sc.direct = cap <= (pairs >= 64 ? 16 : 8) * PG_UNIT;
   sc.N = sc.direct ? (int)pairs : device_sms() * BLOCKS_SM;
   return sc;
 }

@@ -452,9 +452,10 @@ def test_bad_pages_of_split_sequences(dtype, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("hd,h,g", [(64, 4, 2), (128, 20, 2)])
-def test_most_sequences(hd, h, g, dtype, fmt):
-    """8192 sequences, some long, in pages that all of them share."""
+@pytest.mark.parametrize("hd,h,g,cols", [(64, 4, 2, 60), (64, 4, 2, 70), (128, 20, 2, 70)])
+def test_most_sequences(hd, h, g, cols, dtype, fmt):
+    """8192 sequences, some long, in pages that all of them share; tables that
+    are not split and tables that are."""
     import scratch_llama_decoder_b200 as P
     n, ps, n_pages = 8192, 16, 300
     pages, scales = _filled(fmt, n_pages, ps, g, hd, 22)
@@ -463,7 +464,7 @@ def test_most_sequences(hd, h, g, dtype, fmt):
     some = torch.randperm(n, generator=gen)[:24]
     lens[some[:12]] = torch.randint(0, 961, (12,), generator=gen)
     lens[0], lens[-1] = 960, 0
-    table = torch.randint(0, n_pages, (n, 60), generator=gen).to(torch.int32)
+    table = torch.randint(0, n_pages, (n, cols), generator=gen).to(torch.int32)
     q = torch.randn(n, h * hd, device="cuda").to(dtype)
     flag = torch.zeros(1, dtype=torch.int32, device="cuda")
     out, lse = P.attention_paged(q, pages, table.cuda(), lens.to(torch.int32).cuda(),
