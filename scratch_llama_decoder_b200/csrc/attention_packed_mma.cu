@@ -18,7 +18,7 @@
 //
 // The tcgen05 kernels have one or two 128-row items in flight on an SM, each a
 // chain of loads, products, softmax and store: 4 us an item (20 us forward and
-// backward) however few rows it has.  These have 3 to 5 blocks of 64 rows, at a
+// backward) however few rows it has.  These have 2 to 4 blocks of 64 rows, at a
 // third of the rate.  So they win where sequences are short, by the mean of
 // n_rows / n_seq (16384 rows, 8 heads, us, these and tcgen05's):
 //   forward   heads of 32: 64 rows 28, 50; 192: 27, 35; 256: 28, 27
@@ -37,7 +37,7 @@ namespace llm {
 namespace pk_mma {
 
 constexpr int NT = 128, TB = 64;
-// Blocks per SM that registers are cut for.
+// Blocks per SM that registers are cut for (5 at heads of 32: spills, twice the time).
 constexpr int per_sm(int hd) { return hd == 32 ? 4 : hd == 64 ? 3 : 2; }
 template <int HD> constexpr int LD = HD + 8;          // row of a tile
 template <int HD> constexpr int TILE = TB * LD<HD>;  // elements
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(NT, per_sm(HD))
         if (!hf || both)
 #pragma unroll
           for (int k = 0; k < HD / 16; k++) abt_step<HD>(s[hf], qf[k], K, 32 * hf, k);
-      float mn[2] = {m[0], m[1]};
+      float mn[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int hf = 0; hf < 2; hf++)
 #pragma unroll
@@ -180,16 +180,17 @@ __global__ void __launch_bounds__(NT, per_sm(HD))
           for (int e = 0; e < 4; e++) {
             const int key = 32 * hf + 8 * nt + (lane & 3) * 2 + (e & 1);
             float &x = s[hf][nt][e];
-            x = diag && key > row + (e & 2) * 4 ? -INFINITY : x * sl2;
+            if (diag && key > row + (e & 2) * 4) x = -INFINITY;
             mn[e >> 1] = fmaxf(mn[e >> 1], x);
           }
 #pragma unroll
       for (int r = 0; r < 2; r++) {
         mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 1));
         mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xffffffffu, mn[r], 2));
-        const float ref = mn[r] == -INFINITY ? 0.f : mn[r], corr = tc::ex2(m[r] - ref);
-        m[r] = mn[r];
-        l[r] *= corr;
+        const float top = fmaxf(m[r], mn[r] * sl2);
+        const float ref = top == -INFINITY ? 0.f : top, corr = tc::ex2(m[r] - ref);
+        m[r] = top;
+        float2 lr = make_float2(l[r] * corr, 0.f);
 #pragma unroll
         for (int i = 0; i < HD / 8; i++) {
           acc[i][2 * r] *= corr;
@@ -198,12 +199,15 @@ __global__ void __launch_bounds__(NT, per_sm(HD))
 #pragma unroll
         for (int hf = 0; hf < 2; hf++)
 #pragma unroll
-          for (int nt = 0; nt < 4; nt++)
-#pragma unroll
-            for (int e = 2 * r; e < 2 * r + 2; e++) {
-              s[hf][nt][e] = tc::ex2(s[hf][nt][e] - ref);
-              l[r] += s[hf][nt][e];
-            }
+          for (int nt = 0; nt < 4; nt++) {
+            float *x = s[hf][nt] + 2 * r;
+            const float2 y = __ffma2_rn(make_float2(x[0], x[1]), make_float2(sl2, sl2),
+                                        make_float2(-ref, -ref));
+            x[0] = tc::ex2(y.x);
+            x[1] = tc::ex2(y.y);
+            lr = __fadd2_rn(lr, make_float2(x[0], x[1]));
+          }
+        l[r] = lr.x + lr.y;
       }
     }
     wait<0>();
@@ -295,17 +299,30 @@ __global__ void __launch_bounds__(NT, per_sm(HD))
 #pragma unroll
     for (int nt = 0; nt < 4; nt++)
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const bool masked = diag && 32 * hf + 8 * nt + (lane & 3) * 2 + (e & 1) > row + (e & 2) * 4;
-        s[nt][e] = masked ? 0.f : tc::ex2(s[nt][e] * sl2 - L2[e >> 1]);
-        if (masked) dp[nt][e] = 0.f;
+      for (int e = 0; e < 4; e += 2) {
+        const float2 y =
+            __ffma2_rn(make_float2(s[nt][e], s[nt][e + 1]), make_float2(sl2, sl2),
+                       make_float2(-L2[e >> 1], -L2[e >> 1]));
+        s[nt][e] = tc::ex2(y.x);
+        s[nt][e + 1] = tc::ex2(y.y);
+        if (diag) {
+          const int after = 32 * hf + 8 * nt + (lane & 3) * 2 - row - e * 4;  // keys past the row
+          if (after > 0) s[nt][e] = dp[nt][e] = 0.f;
+          if (after > -1) s[nt][e + 1] = dp[nt][e + 1] = 0.f;
+        }
       }
   };
   auto add_dq = [&](float (&s)[4][4], const float (&dp)[4][4], const bf16 *K, int hf) {
 #pragma unroll
     for (int nt = 0; nt < 4; nt++)
 #pragma unroll
-      for (int e = 0; e < 4; e++) s[nt][e] *= dp[nt][e] - Dr[e >> 1];
+      for (int e = 0; e < 4; e += 2) {
+        const float2 y = __fmul2_rn(make_float2(s[nt][e], s[nt][e + 1]),
+                                    __fadd2_rn(make_float2(dp[nt][e], dp[nt][e + 1]),
+                                               make_float2(-Dr[e >> 1], -Dr[e >> 1])));
+        s[nt][e] = y.x;
+        s[nt][e + 1] = y.y;
+      }
     ab<HD>(acc, s, K, 32 * hf);
   };
   auto quad = [&](float &x) {  // the row's sum over the 4 threads that hold it

@@ -24,9 +24,9 @@
 // counter): dealt in a fixed snake the fullest CTA had 6% more at 24 sequences
 // of 16001 rows in all; streams that share K and V (two heads of a kv head, or
 // two blocks of a head) leave one idle where a sequence is short: 16 heads
-// ragged 119 us against 115, 17 rows 8.9 against 7.3.
-// Measured (heads of 64; 128): 2 documents of 16384 rows in all, 8 heads, 224
-// us, 629 TFLOP/s; 2 x 8192 rows, 280 us, 982 TFLOP/s.
+// ragged 119 us against 115.
+// Measured (heads of 64; 128): 2 documents of 16384 rows in all, 8 heads, 213
+// us, 662 TFLOP/s; 2 x 8192 rows, 280 us, 982 TFLOP/s.
 // TMEM: S_A, S_B (128 columns each), O_A, O_B (head size each).  Heads to 64
 // leave room for P beside S (SEP), so S_{j+1} is computed while block j's
 // softmax runs; at head 128 P takes the first half of S's columns, and S_{j+1}
@@ -519,8 +519,8 @@ static bool launch(const PkArgs &a, const PkPlan &p, void *o, float *lse, int *f
       !head_map_store(&mo, o, a.hd, a.H, a.n_rows, 1, dw, 32))
     return false;
   const int64_t items = p.cap * a.H;
-  // one item a block at most: no order to plan (17 rows, 8 heads: 10.3 us with
-  // the plan's kernel, 8.9 without)
+  // one item a block at most: no order to plan (300 rows, 8 heads: 11.3 us with
+  // the plan's kernel, 9.7 without)
   const bool plan = items > device_sms() || a.n_seq > PK_FIND_SEQ;
   const PkView pk{p.n_tiles, plan ? p.tiles : nullptr, a.n_rows, (__nv_bfloat16 *)o, dw, a.cu,
                   a.n_seq, nullptr, 0};
