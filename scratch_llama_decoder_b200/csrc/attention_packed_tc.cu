@@ -78,6 +78,18 @@ LLM_DEV Work work(int4 t, int H, int Hkv) {
   return Work{t.y, t.z, t.w, h, h / (H / Hkv), t.w + 1};
 }
 
+// Maxima that are NaN where an operand is.  exp2_poly2 takes a NaN for -126, so
+// a score that is none has to reach the row through its maximum.
+LLM_DEV float nmax(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+LLM_DEV float nmax3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <int NPAIRS>
 LLM_DEV float2 exp2_some(float2 x, int i) {
   return ((i & 15) * NPAIRS) % 16 < NPAIRS ? exp2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
@@ -365,9 +377,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 128; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], sv[i], sv[i + 1]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-        const bool need = top > m + LAZY;  // true on the first block with a key
+        for (int i = 0; i < 128; i += 2) mx[(i >> 1) & 3] = nmax3(mx[(i >> 1) & 3], sv[i], sv[i + 1]);
+        const float top = nmax(nmax(mx[0], mx[1]), nmax(mx[2], mx[3])) * sl2;
+        // true on the first block with a key, and from a NaN on: it stays in m, l and O
+        const bool need = !(top <= m + LAZY);
         if (j > 0 && __any_sync(0xffffffffu, need)) {
           // O is rescaled after the product of the block before
           if (!(ok = warp_wait(o_done + 8 * x, (cb - 1) & 1, abort_sh, gflag))) break;
@@ -446,7 +459,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // in the 128-byte-swizzle image of the store's boxes
       if (!(ok = warp_wait(o_done + 8 * x, (cb - 1) & 1, abort_sh, gflag))) break;
       fence_after();
-      const float l = l2.x + l2.y, inv = 1.f / l;
+      // a maximum that is not finite has no weights to it (an infinite one leaves
+      // the polynomial's pairs finite): NaN, where finite ones add 0
+      const float l = l2.x + l2.y, none = m - m, inv = 1.f / l + none;
       const int sl = nq % C::QS;
       uint8_t *tile = sQ + (x * C::QS + sl) * C::TILE;
 #pragma unroll
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                       pk.out_ld, hd - 64 * c, lane);
       }
       if (q0 + row < T)
-        lse[w.h * pk.n_rows + w.row0 + q0 + row] = (m + __log2f(l)) * LN2;
+        lse[w.h * pk.n_rows + w.row0 + q0 + row] = (m + __log2f(l) + (m > 0.f ? none : 0.f)) * LN2;
       __syncwarp();
       if (C::QS > 1) {
         st_slot = sl;  // released after the next item's first block
