@@ -200,8 +200,9 @@ typedef struct {
   int32_t *d_flag;
 } llm_kv;
 
-/* Packed rows (d_qkv, ld, dtype, d_cu, n_seq, n_rows, as above) into the cache:
- * row i of sequence s becomes position d_start[s] + i - d_cu[s] (d_start int32
+/* Packed rows (d_qkv, ld, dtype, d_cu, n_seq, n_rows, as above; offsets that
+ * decrease or leave the rows count as mended there, with LLM_PACKED_BAD_CU in the
+ * cache's d_flag) into the cache: row i of sequence s becomes position d_start[s] + i - d_cu[s] (d_start int32
  * [n_seq], null = all 0): a whole prompt, a later part of one, or one new
  * token each.  Two rows written to one place (tables that share a page there)
  * leave it with an undefined mix of both.  llm_kernel_kv_read is the inverse:

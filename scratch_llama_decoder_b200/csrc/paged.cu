@@ -11,7 +11,9 @@
 namespace llm {
 namespace pg {
 
-static inline unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
+__host__ __device__ static inline unsigned cdiv(int64_t a, int64_t b) {
+  return (unsigned)((a + b - 1) / b);
+}
 
 // ------------------------------------------------------------ element types
 // 8 consecutive elements; elements at or past n read as 0.
@@ -186,15 +188,59 @@ LLM_DEV void encode8(const float (&x)[8], float scale, float inv, uint32_t (&c)[
   }
 }
 
-// The sequence that holds packed row i (cu[s] <= i < cu[s + 1]), -1 for none.
-LLM_DEV int seq_of(const int32_t *cu, int n_seq, int64_t i) {
-  int lo = 0, hi = n_seq + 1;  // the first entry above i
+// The sequence that holds packed row i (cu[s] <= i < cu[s + 1]), -1 for none, in
+// offsets that do not decrease.  from: the first entry that may be above i (0, or
+// that above an earlier row, where it is looked for near that); set to it.
+LLM_DEV int seq_of(const int32_t *cu, int n_seq, int64_t i, int &from) {
+  int lo = from, hi = n_seq + 1;  // the first entry above i
+  if (lo > 0)
+    for (int step = 1; lo + step < hi; step *= 2) {
+      if (cu[lo + step - 1] > i) hi = lo + step - 1;
+      else lo += step;
+    }
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (cu[mid] > i) hi = mid;
     else lo = mid + 1;
   }
+  from = lo;
   return lo >= 1 && lo <= n_seq && cu[lo - 1] <= i ? lo - 1 : -1;
+}
+// Whether cu decreases or leaves [0, n_rows] at entry s or every step-th further.
+template <int UNROLL>
+LLM_DEV bool bad_offsets(const int32_t *cu, int n_seq, int64_t n_rows, int s, int step) {
+  bool bad = false;
+#pragma unroll UNROLL
+  for (; s <= n_seq; s += step) {
+    const int a = cu[s], b = s < n_seq ? cu[s + 1] : a;
+    bad |= a < 0 || a > b || a > n_rows;
+  }
+  return bad;
+}
+// seq_of in offsets of any contents, each clamped to [0, n_rows] and raised to
+// the largest before it; *begin: the sequence's.  By a whole warp, a row each.
+LLM_DEV int mended_seq_of(const int32_t *cu, int n_seq, int64_t n_rows, int64_t i, int *begin) {
+  const int lane = threadIdx.x & 31;
+  int s = -1, top = 0;
+  for (int s0 = 0; s0 <= n_seq; s0 += 32) {
+    int c = s0 + lane <= n_seq ? min(max(cu[s0 + lane], 0), (int)n_rows) : 0;
+    c = max(c, top);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c = max(c, t);
+    }
+#pragma unroll 1
+    for (int k = 0; k < min(32, n_seq + 1 - s0); k++) {  // the last offset not above i
+      const int t = __shfl_sync(0xffffffffu, c, k);
+      if (t <= i) {
+        s = s0 + k;
+        *begin = t;
+      }
+    }
+    top = __shfl_sync(0xffffffffu, c, 31);
+  }
+  return s < n_seq ? s : -1;
 }
 // ------------------------------------------------------------ write and read
 // A block takes 32 packed rows.  One warp looks their places up (a chain of
@@ -207,122 +253,253 @@ LLM_DEV int seq_of(const int32_t *cu, int n_seq, int64_t i) {
 // packed row, scattered 64-byte pieces: 39 and 26; rows and heads of a step
 // found by division: 57 and 44.)
 constexpr int RW_ROWS = 32, RW_THREADS = 256, RW_HEADS = 8;
+constexpr int RW_LOOK = RW_THREADS - 32;  // threads that look at the offsets
 constexpr int WU = 4, RU = 2;  // heads in flight: write, read (read with 4: 31 us)
-constexpr int64_t NO_PLACE = -1, NO_SEQUENCE = -2;
-LLM_DEV int64_t place(const KvView &kv, const int32_t *cu, const int32_t *start, int n_seq,
-                      int64_t i) {
-  const int s = seq_of(cu, n_seq, i);
+constexpr int64_t NO_PLACE = -1, NO_SEQUENCE = -2;  // kv_row's; and a row of none
+LLM_DEV int64_t place(const KvView &kv, const int32_t *start, int s, int64_t in) {
   if (s < 0) return NO_SEQUENCE;
-  const int64_t row = kv_row(kv, s, (start ? (int64_t)start[s] : 0) + i - cu[s]);
-  if (row < 0 && kv.flag) atomicOr(kv.flag, PK_BAD_PAGE);
+  const int64_t row = kv_row(kv, s, (start ? (int64_t)start[s] : 0) + in);
   return row < 0 ? NO_PLACE : row;
 }
+// The places of 32 rows from i0 on, by warp 0, a row each: by bisection, which
+// takes offsets that do not decrease, or in the mended ones.
+LLM_DEV void find_places(const KvView &kv, const int32_t *cu, const int32_t *start, int n_seq,
+                         int64_t n_rows, int64_t i0, int64_t *rows, int &from) {
+  const int64_t i = i0 + threadIdx.x;
+  const int s = i < n_rows ? seq_of(cu, n_seq, i, from) : -1;
+  rows[threadIdx.x] = place(kv, start, s, s < 0 ? 0 : i - cu[s]);
+}
+LLM_DEV void find_mended(const KvView &kv, const int32_t *cu, const int32_t *start, int n_seq,
+                         int64_t n_rows, int64_t i0, int64_t *rows) {
+  const int64_t i = i0 + threadIdx.x;
+  int begin = 0;
+  const int s = mended_seq_of(cu, n_seq, n_rows, i, &begin);
+  const int64_t row = i < n_rows ? place(kv, start, s, i - begin) : NO_SEQUENCE;
+  rows[threadIdx.x] = row;
+  if (kv.flag) {
+    if (row == NO_PLACE) atomicOr(kv.flag, PK_BAD_PAGE);
+    if (i == 0) atomicOr(kv.flag, PK_BAD_OFFSETS);
+  }
+}
+LLM_DEV void flag_places(const KvView &kv, const int64_t *rows) {  // of the fast path
+  if (threadIdx.x < 32 && kv.flag && rows[threadIdx.x] == NO_PLACE) atomicOr(kv.flag, PK_BAD_PAGE);
+}
 
-template <typename T, int FMT, int LPH, bool VEC>
-__global__ void __launch_bounds__(RW_THREADS)
+// Rows [i1, end) of this block in the mended offsets, a thread for each row and
+// head.  (Calls of their own, so that they cost the fast path no registers.)
+template <typename T, int FMT>
+__device__ __noinline__ void write_mended(const KvView kv, const T *qkv, int64_t ld,
+                                          const int32_t *cu, const int32_t *start, int n_seq,
+                                          int64_t n_rows, int H, int64_t i1, int64_t end,
+                                          int64_t *rows) {
+  const int first = blockIdx.y * RW_HEADS, heads = min(2 * kv.Hkv, first + RW_HEADS);
+#pragma unroll 1
+  for (int64_t i0 = i1; i0 < end; i0 += RW_ROWS) {
+    __syncthreads();
+    if (threadIdx.x < 32) find_mended(kv, cu, start, n_seq, n_rows, i0, rows);
+    __syncthreads();
+    const int r = threadIdx.x / RW_HEADS, h = first + threadIdx.x % RW_HEADS;
+    if (rows[r] < 0 || h >= heads) continue;
+    const T *src = qkv + (i0 + r) * ld + (int64_t)(H + h) * kv.hd;
+    const int64_t dst = rows[r] + (int64_t)h * kv.ps;
+    float x[8], inv = 0.f, scale = 0.f;
+    uint32_t top = 0;
+    if constexpr (FMT >= KV_E4M3) {
+#pragma unroll 1
+      for (int c = 0; c < kv.hd; c++) top = max(top, __float_as_uint(to_f(src[c])) & 0x7fffffffu);
+      scale = row_scale<FMT>(top, &inv);
+      kv.scales[dst] = scale;
+    }
+#pragma unroll 1
+    for (int c = 0; c < kv.hd; c += 8) {
+      read8(src + c, false, kv.hd - c, x);
+      if constexpr (FMT == KV_F32) {
+        write8(reinterpret_cast<float *>(kv.pages) + dst * kv.hd + c, false, kv.hd - c, x);
+      } else if constexpr (FMT == KV_BF16) {
+        write8(reinterpret_cast<__nv_bfloat16 *>(kv.pages) + dst * kv.hd + c, false, kv.hd - c, x);
+      } else {
+        uint32_t code[2] = {0u, 0u};
+        if (top < 0x7f800000u) encode8<FMT>(x, scale, inv, code);
+        write8(kv.pages + dst * kv.hd + c, false, kv.hd - c, code);
+      }
+    }
+  }
+}
+template <typename T, int FMT>
+__device__ __noinline__ void read_mended(const KvView kv, const int32_t *cu, const int32_t *start,
+                                         int n_seq, int64_t n_rows, T *k, T *v, int64_t i1,
+                                         int64_t end, int64_t *rows) {
+  const int first = blockIdx.y * RW_HEADS, heads = min(2 * kv.Hkv, first + RW_HEADS);
+  const int64_t w = (int64_t)kv.Hkv * kv.hd;
+#pragma unroll 1
+  for (int64_t i0 = i1; i0 < end; i0 += RW_ROWS) {
+    __syncthreads();
+    if (threadIdx.x < 32) find_mended(kv, cu, start, n_seq, n_rows, i0, rows);
+    __syncthreads();
+    const int r = threadIdx.x / RW_HEADS, h = first + threadIdx.x % RW_HEADS;
+    const int64_t row = rows[r], src = row + (int64_t)h * kv.ps;
+    if (row == NO_SEQUENCE || h >= heads) continue;
+    T *dst = (h < kv.Hkv ? k : v - w) + (i0 + r) * w + (int64_t)h * kv.hd;
+    float x[8] = {}, sc = 1.f;
+    if constexpr (FMT >= KV_E4M3) sc = row >= 0 ? kv.scales[src] : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < kv.hd; c += 8) {
+      if (row >= 0) kv_read8<FMT>(kv.pages, src * kv.hd + c, false, kv.hd - c, x);
+      if constexpr (FMT >= KV_E4M3) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) x[j] *= sc;
+      }
+      write8(dst + c, false, kv.hd - c, x);
+    }
+  }
+}
+
+// A block looks whether the offsets are bad while warp 0 searches (MANY, where it
+// takes 32 rows several times: before); where they are, it leaves its rows to
+// write_mended and read_mended.  (Blocks an SM: more registers and fewer blocks
+// were 5 to 15% slower.)
+template <typename T, int FMT, int LPH, bool VEC, bool MANY>
+__global__ void __launch_bounds__(RW_THREADS, FMT < KV_E4M3 && !MANY ? 5 : 4)
     k_write(const KvView kv, const T *__restrict__ qkv, int64_t ld, const int32_t *__restrict__ cu,
             const int32_t *__restrict__ start, int n_seq, int64_t n_rows, int H) {
   __shared__ int64_t rows[RW_ROWS];
-  const int64_t i0 = blockIdx.x * (int64_t)RW_ROWS;
+  const int64_t step = RW_ROWS * cdiv(n_rows, (int64_t)gridDim.x * RW_ROWS);  // MANY
+  const int64_t i1 = blockIdx.x * (MANY ? step : RW_ROWS);
+  const int64_t end = MANY ? min(i1 + step, n_rows) : min(i1 + RW_ROWS, n_rows);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane % LPH) * 8;
   // k heads, then v heads: the pages' own order; RW_HEADS of them a block
   const int first = blockIdx.y * RW_HEADS, heads = min(2 * kv.Hkv, first + RW_HEADS);
-  if (warp == 0)
-    rows[lane] = i0 + lane < n_rows ? place(kv, cu, start, n_seq, i0 + lane) : NO_SEQUENCE;
-  for (int g = warp; g < LPH; g += RW_THREADS / 32) {
-    const int r = g * (32 / LPH) + lane / LPH;
-    const bool in = i0 + r < n_rows && e < kv.hd;
-    const T *src = qkv + (i0 + r) * ld + (int64_t)H * kv.hd + e;
-    for (int h0 = first; h0 < heads; h0 += WU) {
-      float x[WU][8];
+  int from = 0;
+  bool bad = MANY && __syncthreads_or(bad_offsets<8>(cu, n_seq, n_rows, threadIdx.x, RW_THREADS));
+  // the first entries' loads ahead of the rows'
+  const int s1 = !MANY && warp > 0 ? min((int)threadIdx.x - 32, n_seq) : n_seq;
+  const int c0 = MANY ? 0 : cu[s1], c1 = MANY ? 0 : cu[min(s1 + 1, n_seq)];
+  // every warp, before its first use of the places
+  auto meet = [&] {
+    if (MANY) {
+      __syncthreads();
+    } else {
+      bad = c0 < 0 || c0 > c1 || c0 > n_rows;
+      if (warp > 0) bad |= bad_offsets<1>(cu, n_seq, n_rows, s1 + RW_LOOK, RW_LOOK);
+      bad = __syncthreads_or(bad);
+    }
+    if (!bad) flag_places(kv, rows);
+  };
+  int64_t i0 = i1;
+  if (!bad) do {
+    if (warp == 0) find_places(kv, cu, start, n_seq, n_rows, i0, rows, from);
+    for (int g = warp; g < LPH; g += RW_THREADS / 32) {
+      const int r = g * (32 / LPH) + lane / LPH;
+      const bool in = i0 + r < n_rows && e < kv.hd;
+      const T *src = qkv + (i0 + r) * ld + (int64_t)H * kv.hd + e;
+      for (int h0 = first; h0 < heads; h0 += WU) {
+        float x[WU][8];
 #pragma unroll
-      for (int k = 0; k < WU; k++) {
-        if (in && h0 + k < heads) {
-          read8(src + (h0 + k) * kv.hd, VEC, kv.hd - e, x[k]);
-        } else {
+        for (int k = 0; k < WU; k++) {
+          if (in && h0 + k < heads) {
+            read8(src + (h0 + k) * kv.hd, VEC, kv.hd - e, x[k]);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[k][j] = 0.f;
+            for (int j = 0; j < 8; j++) x[k][j] = 0.f;
+          }
         }
-      }
-      if (g == warp && h0 == first) __syncthreads();  // the places are there
-      const int64_t row = rows[r];
-      const bool on = in && row >= 0;
+        if (g == warp && h0 == first) meet();
+        const int64_t row = rows[r];
+        const bool on = in && row >= 0 && !bad;
 #pragma unroll
-      for (int k = 0; k < WU; k++) {
-        if (h0 + k >= heads) break;
-        const int64_t dst = row + (int64_t)(h0 + k) * kv.ps;
-        if constexpr (FMT == KV_F32) {
-          if (on)
-            write8(reinterpret_cast<float *>(kv.pages) + dst * kv.hd + e, VEC, kv.hd - e, x[k]);
-        } else if constexpr (FMT == KV_BF16) {
-          if (on)
-            write8(reinterpret_cast<__nv_bfloat16 *>(kv.pages) + dst * kv.hd + e, VEC, kv.hd - e,
-                   x[k]);
-        } else {
-          uint32_t top = 0;
+        for (int k = 0; k < WU; k++) {
+          if (h0 + k >= heads) break;
+          const int64_t dst = row + (int64_t)(h0 + k) * kv.ps;
+          if constexpr (FMT == KV_F32) {
+            if (on)
+              write8(reinterpret_cast<float *>(kv.pages) + dst * kv.hd + e, VEC, kv.hd - e, x[k]);
+          } else if constexpr (FMT == KV_BF16) {
+            if (on)
+              write8(reinterpret_cast<__nv_bfloat16 *>(kv.pages) + dst * kv.hd + e, VEC, kv.hd - e,
+                     x[k]);
+          } else {
+            uint32_t top = 0;
 #pragma unroll
-          for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(x[k][j]) & 0x7fffffffu);
+            for (int j = 0; j < 8; j++) top = max(top, __float_as_uint(x[k][j]) & 0x7fffffffu);
 #pragma unroll
-          for (int o = 1; o < LPH; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          float inv;
-          const float scale = row_scale<FMT>(top, &inv);
-          uint32_t c[2] = {0u, 0u};
-          if (top < 0x7f800000u) encode8<FMT>(x[k], scale, inv, c);
-          if (on) {
-            write8(kv.pages + dst * kv.hd + e, VEC, kv.hd - e, c);
-            if (e == 0) kv.scales[dst] = scale;
+            for (int o = 1; o < LPH; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float inv;
+            const float scale = row_scale<FMT>(top, &inv);
+            uint32_t c[2] = {0u, 0u};
+            if (top < 0x7f800000u) encode8<FMT>(x[k], scale, inv, c);
+            if (on) {
+              write8(kv.pages + dst * kv.hd + e, VEC, kv.hd - e, c);
+              if (e == 0) kv.scales[dst] = scale;
+            }
           }
         }
       }
     }
-  }
-  if (warp >= LPH) __syncthreads();  // warps without rows
+    if (warp >= LPH) meet();  // warps without rows
+    if (MANY) __syncthreads();  // the places have been read
+    i0 += RW_ROWS;
+  } while (MANY && i0 < end);
+  if (bad) write_mended<T, FMT>(kv, qkv, ld, cu, start, n_seq, n_rows, H, i1, end, rows);
 }
 
 // A row without a place reads as zeros, rows of no sequence are left alone.
-template <typename T, int FMT, int LPH, bool VEC>
-__global__ void __launch_bounds__(RW_THREADS)
+template <typename T, int FMT, int LPH, bool VEC, bool MANY>
+__global__ void __launch_bounds__(RW_THREADS, FMT == KV_INT8 && !MANY ? 8 : 6)
     k_read(const KvView kv, const int32_t *__restrict__ cu, const int32_t *__restrict__ start,
            int n_seq, int64_t n_rows, T *__restrict__ k, T *__restrict__ v) {
   __shared__ int64_t rows[RW_ROWS];
-  const int64_t i0 = blockIdx.x * (int64_t)RW_ROWS;
+  const int64_t step = RW_ROWS * cdiv(n_rows, (int64_t)gridDim.x * RW_ROWS);  // MANY
+  const int64_t i1 = blockIdx.x * (MANY ? step : RW_ROWS);
+  const int64_t end = MANY ? min(i1 + step, n_rows) : min(i1 + RW_ROWS, n_rows);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane % LPH) * 8;
   const int first = blockIdx.y * RW_HEADS, heads = min(2 * kv.Hkv, first + RW_HEADS);
   const int64_t w = (int64_t)kv.Hkv * kv.hd;
-  if (warp == 0)
-    rows[lane] = i0 + lane < n_rows ? place(kv, cu, start, n_seq, i0 + lane) : NO_SEQUENCE;
-  __syncthreads();
-  for (int g = warp; g < LPH; g += RW_THREADS / 32) {
-    const int r = g * (32 / LPH) + lane / LPH;
-    const int64_t row = rows[r];
-    if (row == NO_SEQUENCE || e >= kv.hd) continue;
-    T *kd = k + (i0 + r) * w + e, *vd = v + (i0 + r) * w - w + e;  // v of head h - Hkv
-    for (int h0 = first; h0 < heads; h0 += RU) {
-      float x[RU][8], sc[RU];
+  int from = 0;
+  bool bad = MANY && __syncthreads_or(bad_offsets<8>(cu, n_seq, n_rows, threadIdx.x, RW_THREADS));
+  int64_t i0 = i1;
+  if (!bad) do {
+    if (warp == 0) find_places(kv, cu, start, n_seq, n_rows, i0, rows, from);
+    if (MANY)
+      __syncthreads();
+    else
+      bad = __syncthreads_or(warp > 0 &&
+                             bad_offsets<4>(cu, n_seq, n_rows, threadIdx.x - 32, RW_LOOK));
+    if (!bad) flag_places(kv, rows);
+    for (int g = bad ? LPH : warp; g < LPH; g += RW_THREADS / 32) {
+      const int r = g * (32 / LPH) + lane / LPH;
+      const int64_t row = rows[r];
+      if (row == NO_SEQUENCE || e >= kv.hd) continue;
+      T *kd = k + (i0 + r) * w + e, *vd = v + (i0 + r) * w - w + e;  // v of head h - Hkv
+      for (int h0 = first; h0 < heads; h0 += RU) {
+        float x[RU][8], sc[RU];
 #pragma unroll
-      for (int m = 0; m < RU; m++) {
-        sc[m] = 1.f;
-        if (row >= 0 && h0 + m < heads) {
-          const int64_t src = row + (int64_t)(h0 + m) * kv.ps;
-          kv_read8<FMT>(kv.pages, src * kv.hd + e, VEC, kv.hd - e, x[m]);
-          if constexpr (FMT >= KV_E4M3) sc[m] = kv.scales[src];
-        } else {
+        for (int m = 0; m < RU; m++) {
+          sc[m] = 1.f;
+          if (row >= 0 && h0 + m < heads) {
+            const int64_t src = row + (int64_t)(h0 + m) * kv.ps;
+            kv_read8<FMT>(kv.pages, src * kv.hd + e, VEC, kv.hd - e, x[m]);
+            if constexpr (FMT >= KV_E4M3) sc[m] = kv.scales[src];
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[m][j] = 0.f;
+            for (int j = 0; j < 8; j++) x[m][j] = 0.f;
+          }
         }
-      }
 #pragma unroll
-      for (int m = 0; m < RU; m++) {
-        const int h = h0 + m;
-        if (h >= heads) break;
-        if constexpr (FMT >= KV_E4M3) {
+        for (int m = 0; m < RU; m++) {
+          const int h = h0 + m;
+          if (h >= heads) break;
+          if constexpr (FMT >= KV_E4M3) {
 #pragma unroll
-          for (int j = 0; j < 8; j++) x[m][j] *= sc[m];
+            for (int j = 0; j < 8; j++) x[m][j] *= sc[m];
+          }
+          write8((h < kv.Hkv ? kd : vd) + (int64_t)h * kv.hd, VEC, kv.hd - e, x[m]);
         }
-        write8((h < kv.Hkv ? kd : vd) + (int64_t)h * kv.hd, VEC, kv.hd - e, x[m]);
       }
     }
-  }
+    if (MANY) __syncthreads();  // the places have been read
+    i0 += RW_ROWS;
+  } while (MANY && i0 < end);
+  if (bad) read_mended<T, FMT>(kv, cu, start, n_seq, n_rows, k, v, i1, end, rows);
 }
 
 // --------------------------------------------------------------- attention
@@ -1291,15 +1468,24 @@ static int64_t pre_bytes(int n_seq) { return (4 * ((int64_t)n_seq + 1) + 255) / 
 }  // namespace pg
 
 namespace pg {
-static dim3 rw_grid(const KvView &kv, int64_t n_rows) {
-  return dim3(cdiv(n_rows, RW_ROWS), cdiv(2 * kv.Hkv, RW_HEADS));
+// A block for each 32 rows and RW_HEADS heads; where there are so many sequences
+// that a block's look through their offsets costs as much as its rows, 8 blocks
+// an SM with several times 32 rows each (2048 sequences, bfloat16 written: a
+// block each 26 us, 8 an SM 33; 8192 sequences: 46 and 33).
+constexpr int RW_SEQS = 4096;
+static dim3 rw_grid(const KvView &kv, int64_t n_rows, bool many) {
+  const unsigned x = cdiv(n_rows, RW_ROWS), y = cdiv(2 * kv.Hkv, RW_HEADS);
+  const unsigned most = max(8 * device_sms() / y, 1u);
+  return dim3(many && x > most ? most : x, y);
 }
-// Calls f with the element type, cache format, lanes of a head and vector
-// access as constants.
+// Calls f with the element type, cache format, lanes of a head, vector access
+// and MANY as constants (rows without vector access: the MANY kernels for all).
 template <typename F>
-static void rw_dispatch(DType dt, int fmt, int hd, bool vec, F f) {
+static void rw_dispatch(DType dt, int fmt, int hd, bool vec, bool many, F f) {
+  const std::true_type yes;
+  const std::false_type no;
   auto with = [&](auto t, auto m, auto l) {
-    vec ? f(t, m, l, std::true_type()) : f(t, m, l, std::false_type());
+    !vec ? f(t, m, l, no, yes) : many ? f(t, m, l, yes, yes) : f(t, m, l, yes, no);
   };
   auto lanes = [&](auto t, auto m) {
     if (hd <= 8) with(t, m, std::integral_constant<int, 1>());
@@ -1326,10 +1512,11 @@ void kv_write(const KvView &kv, const void *qkv, int64_t ld, DType dt, const int
   using namespace pg;
   const bool vec = kv.hd % 8 == 0 && ld % 8 == 0 && !((uintptr_t)qkv & 15) &&
                    !((uintptr_t)kv.pages & 15);
-  rw_dispatch(dt, kv.fmt, kv.hd, vec, [&](auto t, auto m, auto l, auto v) {
+  const bool many = n_seq > RW_SEQS;
+  rw_dispatch(dt, kv.fmt, kv.hd, vec, many, [&](auto t, auto m, auto l, auto x, auto n) {
     using T = decltype(t);
-    k_write<T, decltype(m)::value, decltype(l)::value, decltype(v)::value>
-        <<<rw_grid(kv, n_rows), RW_THREADS, 0, s>>>(kv, (const T *)qkv, ld, cu, start, n_seq,
+    k_write<T, decltype(m)::value, decltype(l)::value, decltype(x)::value, decltype(n)::value>
+        <<<rw_grid(kv, n_rows, many), RW_THREADS, 0, s>>>(kv, (const T *)qkv, ld, cu, start, n_seq,
                                                       n_rows, H);
   });
   count_launch();
@@ -1339,10 +1526,11 @@ void kv_read(const KvView &kv, const int32_t *cu, const int32_t *start, int n_se
              void *k, void *v, DType dt, cudaStream_t s) {
   using namespace pg;
   const bool vec = kv.hd % 8 == 0 && !(((uintptr_t)k | (uintptr_t)v | (uintptr_t)kv.pages) & 15);
-  rw_dispatch(dt, kv.fmt, kv.hd, vec, [&](auto t, auto m, auto l, auto x) {
+  const bool many = n_seq > RW_SEQS;
+  rw_dispatch(dt, kv.fmt, kv.hd, vec, many, [&](auto t, auto m, auto l, auto x, auto n) {
     using T = decltype(t);
-    k_read<T, decltype(m)::value, decltype(l)::value, decltype(x)::value>
-        <<<rw_grid(kv, n_rows), RW_THREADS, 0, s>>>(kv, cu, start, n_seq, n_rows, (T *)k,
+    k_read<T, decltype(m)::value, decltype(l)::value, decltype(x)::value, decltype(n)::value>
+        <<<rw_grid(kv, n_rows, many), RW_THREADS, 0, s>>>(kv, cu, start, n_seq, n_rows, (T *)k,
                                                       (T *)v);
   });
   count_launch();

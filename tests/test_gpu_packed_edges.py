@@ -62,3 +62,89 @@ def test_one_key_that_is_not_finite(what, rows, hd, dtype):
             O = w @ v
             ref.check(o, O, rel[:, None] * (w @ v.abs()) + r * O.abs() + 1e-30, (s, i, "out"))
             ref.check(l, L, es + ex + (rows + 8) * u + 4 * u * L.abs() + 1e-30, (s, i, "lse"))
+
+
+def _bad_offsets(n, n_seq, seed):
+    """Offsets that decrease or leave [0, n] in several places, and the same
+    clamped and raised to the largest before them."""
+    gen = torch.Generator().manual_seed(seed)
+    bad = torch.sort(torch.randint(0, n + 1, (n_seq + 1,), generator=gen))[0].tolist()
+    bad[0], bad[n_seq // 2], bad[n_seq // 2 - 1] = -3, -(1 << 31), n // 2 + 1
+    if n_seq > 6:
+        bad[5], bad[-1] = 1, (1 << 31) - 1
+    good, top = [], 0
+    for c in bad:
+        top = max(top, min(max(c, 0), n))
+        good.append(top)
+    return bad, good
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd,g", [(64, 2), (128, 5), (6, 1)])
+@pytest.mark.parametrize("n,n_seq", [(100, 3), (33, 40), (5000, 300), (20000, 5000), (300, 65536),
+                                     (700, 1025)])
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "e4m3", "int8"])
+def test_cache_offsets_count_as_mended(fmt, n, n_seq, hd, g, dtype):
+    """kv_write and kv_read take bad offsets as attention_packed does, and say
+    so in the flag."""
+    import scratch_llama_decoder_b200 as P
+    h, ps = g, 8
+    gen = torch.Generator(device="cuda").manual_seed(32)
+    qkv = torch.randn(n, (h + 2 * g) * hd, generator=gen, device="cuda").to(dtype)
+    for bad, good in (_bad_offsets(n, n_seq, 33), ([0, 60, 20, 100], [0, 60, 60, 100])):
+        if good[-1] > n:
+            continue
+        lens = [b - a for a, b in zip(good[:-1], good[1:])]
+        starts = [i % 11 for i in range(len(lens))]
+        need = [-(-(a + x) // ps) if x else 0 for a, x in zip(starts, lens)]
+        cols = max(need)
+        table = torch.full((len(lens), cols), -1, dtype=torch.int32)
+        at = 0
+        for s, x in enumerate(need):
+            table[s, :x] = torch.arange(at, at + x)
+            at += x
+        table = table.cuda()
+        st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        got = []
+        for cu in (bad, good):
+            pages, scales = P.kv_pages(at, ps, g, hd, fmt)
+            flag = torch.zeros(3, dtype=torch.int32, device="cuda")
+            cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            k, v = (torch.full((n, g, hd), 9.0, device="cuda").to(dtype) for _ in range(2))
+            P.kv_write(qkv, cut, h, pages, table, scales=scales, starts=st, flag=flag[:1])
+            P.kv_read(pages, table, cut, n, dtype, scales=scales, starts=st, k=k, v=v,
+                      flag=flag[1:2])
+            P.kv_write(qkv, cut, h, pages, table, scales=scales, starts=st, flag=flag[2:])
+            assert flag.tolist() == [int(cu is bad)] * 3
+            got.append((pages, scales, k, v))
+        for a, b in zip(*got):
+            assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        # in a sequence: the stored values, rounded to dtype; elsewhere as it was
+        k, lo, hi = got[1][2], good[0], good[-1]
+        want, _ = ref.stored(qkv.view(n, h + 2 * g, hd)[:, h:h + g], fmt)
+        tol = max(ref.R[dtype], ref.U) * want.abs()
+        assert bool(((k.double() - want).abs() <= tol)[lo:hi].all())
+        assert bool((k[:lo] == 9).all() and (k[hi:] == 9).all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_cache_of_the_most_sequences(fmt):
+    """65536 sequences of 16 rows each: written and read whole."""
+    import scratch_llama_decoder_b200 as P
+    n, n_seq, g, hd, ps = 1 << 20, 65536, 1, 32, 16
+    gen = torch.Generator(device="cuda").manual_seed(34)
+    qkv = torch.randn(n, 3 * hd, generator=gen, device="cuda").bfloat16()
+    cut = torch.arange(0, n + 1, 16, dtype=torch.int32, device="cuda")
+    pages, scales = P.kv_pages(n_seq, ps, g, hd, fmt)
+    table = torch.randperm(n_seq, generator=gen, device="cuda").to(torch.int32)[:, None]
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    P.kv_write(qkv, cut, 1, pages, table, scales=scales, flag=flag)
+    k, v = P.kv_read(pages, table, cut, n, torch.bfloat16, scales=scales, flag=flag)
+    assert int(flag) == 0
+    for got, x in ((k, qkv[:, hd:2 * hd]), (v, qkv[:, 2 * hd:])):
+        if fmt == "bf16":
+            assert torch.equal(got[:, 0], x)
+        else:
+            want, _ = ref.stored(x, fmt)
+            # the code's value, rounded to bfloat16
+            assert bool(((got[:, 0].double() - want).abs() <= 2.0 ** -8 * want.abs()).all())
