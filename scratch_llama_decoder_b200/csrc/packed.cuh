@@ -59,6 +59,15 @@ inline PkPlan pk_plan(void *ws, int64_t n_rows, int n_seq, int H, bool backward)
 // sequence + 1 or 0 for no such tile}.
 LLM_DEV int4 pk_find(const int32_t *cu, int n_seq, int n_rows, int block, int k, int *flag) {
   const int lane = threadIdx.x & 31;
+  if (k == 0 && flag) {  // the first tile's block looks at all, the others to their tile
+    bool bad = false;
+#pragma unroll 4
+    for (int s = 32 + lane; s < n_seq; s += 32) {
+      const int a = cu[s], b = cu[s + 1];
+      bad |= a < 0 || a > b || b > n_rows;
+    }
+    if (bad) atomicOr(flag, PK_BAD_OFFSETS);
+  }
   int top = 0;  // the largest offset so far
   for (int s0 = 0; s0 < n_seq; s0 += 32) {
     const int s = min(s0 + lane, n_seq - 1);

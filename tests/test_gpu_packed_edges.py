@@ -148,3 +148,33 @@ def test_cache_of_the_most_sequences(fmt):
             want, _ = ref.stored(x, fmt)
             # the code's value, rounded to bfloat16
             assert bool(((got[:, 0].double() - want).abs() <= 2.0 ** -8 * want.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hd", [32, 64, 128, 20])
+@pytest.mark.parametrize("n,n_seq,cu,bad", [
+    (1, 40, [0] + [1] * 40, {36: -9}),
+    (20, 40, list(range(21)) + [20] * 20, {35: 3}),
+    (20, 200, list(range(21)) + [20] * 180, {199: 21}),
+    (20, 40, list(range(21)) + [20] * 20, {40: 7}),
+    (6000, 40, list(range(0, 6001, 600)) + [6000] * 30, {35: 5999}),
+])
+def test_bad_offsets_behind_the_last_row_are_flagged(n, n_seq, cu, bad, hd, dtype):
+    """Offsets that no row needs, past those of every tile: reported, and
+    the outputs as without them."""
+    import scratch_llama_decoder_b200 as P
+    gen = torch.Generator(device="cuda").manual_seed(35)
+    qkv = torch.randn(n, 3 * hd, generator=gen, device="cuda").to(dtype)
+    dout = torch.randn(n, hd, generator=gen, device="cuda").to(dtype)
+    res = []
+    for broken in (False, True):
+        c = list(cu)
+        for i, x in (bad if broken else {}).items():
+            c[i] = x
+        flags = torch.zeros(2, dtype=torch.int32, device="cuda")
+        cut = torch.tensor(c, dtype=torch.int32, device="cuda")
+        out, lse = P.attention_packed(qkv, cut, 1, 1, flag=flags[:1])
+        dx = P.attention_packed_backward(qkv, cut, 1, 1, out, lse, dout, flag=flags[1:])
+        assert flags.tolist() == [int(broken)] * 2
+        res.append((out, lse, dx))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
