@@ -29,8 +29,9 @@ _i32, _f32 = torch.int32, torch.float32
 _KV = struct.Struct("@PPPqqiiiiiP")
 assert _KV.size == C.sizeof(L.llm_kv)
 # The current stream's handle as an integer: torch.cuda.current_stream() builds
-# a Stream object for it (2 us of a call whose kernel takes 5).
-_stream = torch._C._cuda_getCurrentRawStream
+# a Stream object for it (2 us of a call whose kernel takes 5).  A torch built
+# without CUDA has none, and no tensors that a call gets as far as this with.
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current = torch.cuda.current_device
 _empty = torch.empty
 _packed_fwd = L.lib.llm_kernel_attention_packed_fwd
