@@ -7,6 +7,10 @@ with their arguments taken from tensors.  Every call checks its tensors
 enqueues on the current stream of the tensors' device; nothing synchronises.
 Inputs must be ready on that stream, as for any torch operation.
 
+Nothing is recorded for autograd: outputs carry no gradient whatever the inputs
+require (attention_packed and attention_paged warn where an input asks for one);
+the gradient of attention_packed is attention_packed_backward's.
+
 `flag`, where a call takes it, is an int32 tensor of one element on the same
 device: error bits (LLM_PACKED_BAD_CU, LLM_KV_BAD_PAGE, LLM_PACKED_TIMEOUT)
 are OR-ed into it on the device and never cleared.
@@ -14,6 +18,7 @@ are OR-ed into it on the device and never cleared.
 import ctypes as C
 import functools
 import struct
+import warnings
 
 import torch
 
@@ -42,6 +47,12 @@ _paged = L.lib.llm_kernel_attention_paged
 
 def _bad(what):
     raise ValueError(what)
+
+
+def _unrecorded(name, t, what):
+    if t.requires_grad and torch.is_grad_enabled():
+        warnings.warn(f"{name} records nothing for autograd: its outputs carry no gradient of "
+                      f"{what}; pass {what}.detach(), or call it under torch.no_grad()", stacklevel=3)
 
 
 def _on(i, fn, *args):
@@ -127,6 +138,7 @@ def attention_packed(qkv, cu_seqlens, n_head, n_kv_head, out=None, lse=None, fla
     type, lse float32 [n_head, rows]); rows of no sequence keep what out and
     lse held (nothing useful unless they are given)."""
     dt, i, ld = _rows("qkv", qkv)
+    _unrecorded("attention_packed", qkv, "qkv")
     n_rows, width = qkv.shape
     hd, dev = _head_dim(width, n_head, n_kv_head), qkv.device
     cu, n_seq = _offsets(cu_seqlens, i)
@@ -284,6 +296,7 @@ def attention_paged(q, pages, table, lens, scales=None, out=None, lse=None, flag
     and lse -inf."""
     kv, i, g, hd, ps, cols = _kv(pages, scales, table, flag)
     dt, qi, ld = _rows("q", q)
+    _unrecorded("attention_paged", q, "q")
     n_seq, width = q.shape
     n_head = width // hd if hd else 0
     if qi != i or not hd or width % hd or not g or n_head % g:

@@ -178,3 +178,32 @@ def test_bad_offsets_behind_the_last_row_are_flagged(n, n_seq, cu, bad, hd, dtyp
         assert flags.tolist() == [int(broken)] * 2
         res.append((out, lse, dx))
     assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+def test_gradients_that_nothing_records_are_told():
+    """Inputs that require a gradient: a warning, the same outputs, none of
+    them with a gradient; no warning where none is asked for."""
+    import warnings
+
+    import scratch_llama_decoder_b200 as P
+    h, g, hd = 2, 1, 32
+    qkv = torch.randn(9, (h + 2 * g) * hd, device="cuda")
+    cu = torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda")
+    pages, _ = P.kv_pages(2, 8, g, hd, "f32")
+    table = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([4, 5], dtype=torch.int32, device="cuda")
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        want = P.attention_packed(qkv, cu, h, g)
+        P.kv_write(qkv, cu, h, pages, table)
+        paged = P.attention_paged(qkv[[3, 8], :h * hd], pages, table, lens)
+        leaf = qkv.clone().requires_grad_()
+        with torch.no_grad():
+            P.attention_packed(leaf, cu, h, g)
+        P.attention_packed_backward(leaf, cu, h, g, *want, torch.ones_like(want[0]))
+    with pytest.warns(UserWarning, match="attention_packed records nothing"):
+        got = P.attention_packed(leaf, cu, h, g)
+    with pytest.warns(UserWarning, match="attention_paged records nothing"):
+        one = P.attention_paged(leaf[[3, 8], :h * hd], pages, table, lens)
+    for a, b in zip((*want, *paged), (*got, *one)):
+        assert torch.equal(a, b) and not b.requires_grad
