@@ -136,7 +136,8 @@ int llm_kernel_embed_bwd_noalloc(const int32_t *d_tokens, const float *d_dx, flo
  *     [n_head, n_rows], the natural-log sum of exp of each row's scores.
  *   Backward: from d_o, d_lse and d_dout (like d_o) writes d_dqkv (rows of
  *     dqkv_ld elements, the first qkvw of them written), no atomics: the same
- *     inputs give the same bits.  d_dqkv overlaps no input.
+ *     inputs give the same bits.  d_dqkv shares no byte with an input
+ *     (LLM_ERR_ARG), as d_o and d_lse share none with d_qkv.
  *   d_ws: at least llm_kernel_attention_packed_workspace() bytes, 16-byte
  *     aligned, no initialisation needed; used while the call's kernels run, so
  *     calls that may overlap on the GPU need one each.

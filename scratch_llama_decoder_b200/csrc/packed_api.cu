@@ -2,6 +2,7 @@
 // the host, then the launches.
 #include "../../include/llm.h"
 #include "../../include/llm_kernels.h"
+#include "overlap.h"
 #include "paged.cuh"
 
 using namespace llm;
@@ -108,8 +109,16 @@ int llm_kernel_attention_packed_bwd(const void *d_qkv, int64_t ld, int dtype, co
   const PkPlan p = pk_plan(d_ws, n_rows, n_seq, n_head, true);
   const int e = elem(dtype);
   if (!aligned(d_o, e) || !aligned(d_lse, 4) || !aligned(d_dout, e) || !aligned(d_dqkv, e) ||
-      !aligned(d_ws, 16) || ws_bytes < p.bytes || d_dqkv == d_qkv || d_dqkv == d_o ||
-      d_dqkv == d_dout)
+      !aligned(d_ws, 16) || ws_bytes < p.bytes)
+    return LLM_ERR_ARG;
+  // d_dqkv overlaps no input: its rows are written while those are still read
+  const int64_t w = (int64_t)(n_head + 2 * n_kv_head) * head_dim * e,
+                on = n_rows * n_head * head_dim * e;
+  const uintptr_t dx = (uintptr_t)d_dqkv;
+  if (rows_overlap(d_dqkv, dqkv_ld * e, d_qkv, ld * e, w, n_rows) ||
+      overlap(dx, dqkv_ld * e, w, n_rows, (uintptr_t)d_o, on) ||
+      overlap(dx, dqkv_ld * e, w, n_rows, (uintptr_t)d_dout, on) ||
+      overlap(dx, dqkv_ld * e, w, n_rows, (uintptr_t)d_lse, 4 * n_rows * n_head))
     return LLM_ERR_ARG;
   if (!claim_device(nullptr)) return LLM_ERR_ARG;
   g_launches = 0;
