@@ -359,7 +359,7 @@ __device__ __noinline__ void read_mended(const KvView kv, const int32_t *cu, con
 // write_mended and read_mended.  (Blocks an SM: more registers and fewer blocks
 // were 5 to 15% slower.)
 template <typename T, int FMT, int LPH, bool VEC, bool MANY>
-__global__ void __launch_bounds__(RW_THREADS, FMT < KV_E4M3 && !MANY ? 5 : 4)
+__global__ void __launch_bounds__(RW_THREADS, FMT < KV_E4M3 && !MANY && LPH < 16 ? 5 : 4)
     k_write(const KvView kv, const T *__restrict__ qkv, int64_t ld, const int32_t *__restrict__ cu,
             const int32_t *__restrict__ start, int n_seq, int64_t n_rows, int H) {
   __shared__ int64_t rows[RW_ROWS];
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(RW_THREADS, FMT < KV_E4M3 && !MANY ? 5 : 4)
 
 // A row without a place reads as zeros, rows of no sequence are left alone.
 template <typename T, int FMT, int LPH, bool VEC, bool MANY>
-__global__ void __launch_bounds__(RW_THREADS, FMT == KV_INT8 && !MANY ? 8 : 6)
+__global__ void __launch_bounds__(RW_THREADS, FMT == KV_INT8 && VEC && !MANY ? 8 : 6)
     k_read(const KvView kv, const int32_t *__restrict__ cu, const int32_t *__restrict__ start,
            int n_seq, int64_t n_rows, T *__restrict__ k, T *__restrict__ v) {
   __shared__ int64_t rows[RW_ROWS];
@@ -1479,13 +1479,14 @@ static dim3 rw_grid(const KvView &kv, int64_t n_rows, bool many) {
   return dim3(many && x > most ? most : x, y);
 }
 // Calls f with the element type, cache format, lanes of a head, vector access
-// and MANY as constants (rows without vector access: the MANY kernels for all).
+// and MANY as constants.
 template <typename F>
 static void rw_dispatch(DType dt, int fmt, int hd, bool vec, bool many, F f) {
   const std::true_type yes;
   const std::false_type no;
   auto with = [&](auto t, auto m, auto l) {
-    !vec ? f(t, m, l, no, yes) : many ? f(t, m, l, yes, yes) : f(t, m, l, yes, no);
+    vec ? many ? f(t, m, l, yes, yes) : f(t, m, l, yes, no)
+        : many ? f(t, m, l, no, yes) : f(t, m, l, no, no);
   };
   auto lanes = [&](auto t, auto m) {
     if (hd <= 8) with(t, m, std::integral_constant<int, 1>());
