@@ -147,6 +147,12 @@ int llm_kernel_embed_bwd_noalloc(const int32_t *d_tokens, const float *d_dx, flo
  *     nothing outside the rows is touched -- and bit 4 (LLM_PACKED_TIMEOUT)
  *     when a bounded wait of the tensor-core kernels gave up (the outputs are
  *     incomplete).  Never cleared here.
+ * Which kernels run goes by n_rows / n_seq (empty sequences and rows of none
+ * count), and in a captured call stays as it was captured: every choice serves
+ * any offsets, but a long sequence among so many empty or short ones that the
+ * mean is short (to 64 rows; 128 to 320 for small calls, heads to 32 and the
+ * backward) runs at a half to a quarter of its rate.  Offsets padded to more
+ * sequences than there are cost that where the rows are few.
  * A value that is not finite reaches rows of its own sequence only: in the
  * forward those behind it, and of those before it any in the same 128 rows of
  * the sequence; in the backward any of them.
@@ -201,15 +207,16 @@ typedef struct {
   int32_t *d_flag;
 } llm_kv;
 
-/* Packed rows (d_qkv, ld, dtype, d_cu, n_seq, n_rows, as above; offsets that
- * decrease or leave the rows count as mended there, with LLM_PACKED_BAD_CU in the
- * cache's d_flag) into the cache: row i of sequence s becomes position d_start[s] + i - d_cu[s] (d_start int32
+/* Packed rows (d_qkv, ld, dtype, d_cu, n_seq, n_rows, as above) into the cache:
+ * row i of sequence s becomes position d_start[s] + i - d_cu[s] (d_start int32
  * [n_seq], null = all 0): a whole prompt, a later part of one, or one new
- * token each.  Two rows written to one place (tables that share a page there)
- * leave it with an undefined mix of both.  llm_kernel_kv_read is the inverse:
- * d_k, d_v [n_rows, n_kv_head, head_dim] of dtype get the values of those
- * positions (rows without a place as zeros; rows of no sequence are left as
- * they were).  Limits as above; LLM_ERR_ARG otherwise. */
+ * token each.  Offsets that decrease or leave the rows count as mended, as
+ * above, with LLM_PACKED_BAD_CU in the cache's d_flag.  Two rows written to one
+ * place (tables that share a page there) leave it with an undefined mix of both.
+ * llm_kernel_kv_read is the inverse: d_k, d_v [n_rows, n_kv_head, head_dim] of
+ * dtype get the values of those positions (rows without a place as zeros; rows
+ * of no sequence are left as they were).  Limits as above; LLM_ERR_ARG
+ * otherwise. */
 int llm_kernel_kv_write(const llm_kv *kv, const void *d_qkv, int64_t ld, int dtype,
                         const int32_t *d_cu, const int32_t *d_start, int n_seq, int64_t n_rows,
                         int n_head, void *stream);

@@ -145,7 +145,7 @@ LLM_DEV float ex2(float x) {
 // under half a bf16 ulp); 2^k applied by adding k to the exponent field.
 // Domain x <= 126 (the softmax loops pass x <= 8); x is clamped below at
 // -126, where the result is a tiny positive number (under 2^-125) rather
-// than 0.
+// than 0; so is a NaN.
 constexpr float EXP2_C0 = 0.9999280571937561f, EXP2_C1 = 0.6932609677314758f,
                 EXP2_C2 = 0.2426111251115799f, EXP2_C3 = 0.0551716685295105f;
 LLM_DEV float2 exp2_poly2(float2 x) {
